@@ -264,6 +264,88 @@ DG_API dg_status_t dg_m_grouped_bf16_gemm_nt_masked(const void *a, const void *b
                                                     int N, int K, void *stream);
 
 /*
+ * Ragged M-grouped BF16 products (page 2 "MoE模型专属优化": M-grouped GEMMs; the
+ * pages know only padded layouts): the tokens of all experts packed back to
+ * back, without padding, as a router's sort leaves them.
+ *   m_offsets [G + 1] int32 on the device: expert g owns the rows
+ *             m_offsets[g] <= m < m_offsets[g + 1] of a and d; an expert may own
+ *             none.  0 <= m_offsets[0] <= ... <= m_offsets[G] <= M_total.  Only the
+ *             device reads them (graph-compatible).
+ *   Rows outside [m_offsets[0], m_offsets[G]) reach no result and are not
+ *             written.  Offsets out of order or range are recorded as
+ *             DG_ERR_INVALID_VALUE in the device status word; the kernel then
+ *             uses them clamped to [0, M_total] and raised to the largest before.
+ * Sums are FP32, d is BF16 (RNE).  M_total >= 0; K, N > 0 and multiples of 8;
+ * 1 <= G <= 1024.  a and d may be NULL when M_total == 0 (a no-op).  Sizes whose
+ * number of 128 x 64 tiles passes 2^31 are DG_ERR_UNSUPPORTED_SHAPE.
+ *
+ * Forward:  a [M_total, K], b [G, N, K] (K-major), d [M_total, N]:
+ *   D[m,n] = sum_k A[m,k] * B[g(m)][n,k]
+ */
+DG_API dg_status_t dg_m_grouped_bf16_gemm_nt_ragged(const void *a, const void *b, void *d,
+                                                    const int32_t *m_offsets, int M_total, int N,
+                                                    int K, int G, void *stream);
+
+/* The input gradient of the product above, from the same weights as they lie:
+ * a [M_total, K] is the output's gradient, b [G, K, N] the forward's weights
+ * (its N is this call's K), d [M_total, N]:
+ *   D[m,n] = sum_k A[m,k] * B[g(m)][k,n] */
+DG_API dg_status_t dg_m_grouped_bf16_gemm_nn_ragged(const void *a, const void *b, void *d,
+                                                    const int32_t *m_offsets, int M_total, int N,
+                                                    int K, int G, void *stream);
+
+/*
+ * Ragged K-grouped BF16 product, the weight gradient of the products above
+ * (page 3 "核心功能": k_grouped_gemm), with both operands as they lie in the
+ * token buffers:
+ *   D[g][m,n] = sum_{k_offsets[g] <= k < k_offsets[g+1]} A[k,m] * B[k,n]
+ *   a [K_total, M] BF16 (the output's gradient), b [K_total, N] BF16 (the input),
+ *   d [G, M, N], FP32 (d_is_fp32 != 0) or BF16.
+ * accumulate == 0: d is fully written (zeros for an expert without tokens);
+ * otherwise the sums are added to what d holds (a micro-batch's gradient on top
+ * of the earlier ones; BF16: added in FP32, rounded once).
+ * k_offsets as m_offsets above, over K_total; tokens outside [k_offsets[0],
+ * k_offsets[G]) reach no result, whatever they hold.
+ * FP32 results are summed in FP32 with rounding (the tensor core's own sums,
+ * which truncate, run over 512 tokens at a time).  M, N > 0 and multiples of 8;
+ * 1 <= G <= 1024.  K_total == 0 writes zeros (accumulate: a no-op); a and b may
+ * then be NULL.  Results do not depend on the order of execution.
+ */
+DG_API dg_status_t dg_k_grouped_bf16_gemm_tn_ragged(const void *a, const void *b, void *d,
+                                                    int d_is_fp32, const int32_t *k_offsets, int G,
+                                                    int M, int N, int K_total, int accumulate,
+                                                    void *stream);
+
+/*
+ * Products of a few BF16 rows with 4-bit weights (page 3 "核心功能" lists 4-bit
+ * formats; here integer codes with group scales, the decode step's weights):
+ *   D[m,n] = sum_j s[j,n] * sum_{k in group j} (q[n,k] - z[j,n]) * x[m,k]
+ *   x      [M, K] BF16, d [M, N] BF16 (RNE of the FP32 sum)
+ *   w      [N, K/2] codes 0..15: byte [n][k/2] holds k even in its low four bits
+ *          and k + 1 in its high four
+ *   scales [K/group_size, N] BF16 ("MN-major"): of row n and the group of
+ *          group_size consecutive k
+ *   zeros  [K/group_size, N] uint8, 0..127, or NULL for 8 everywhere
+ * q - z is exact and the scale is applied to the group's FP32 sum, so no weight
+ * is rounded.  group_size 32, 64 or 128, K % group_size == 0, N % 8 == 0,
+ * N <= 65535 * 128.  Any M: rows are taken up to 32 at a time and the weights
+ * read once for each such run, so the call is meant for few.  M == 0 is a no-op
+ * (x and d may be NULL).
+ */
+DG_API dg_status_t dg_w4_gemv_nt(const void *x, const uint8_t *w, const void *scales,
+                                 const uint8_t *zeros, void *d, int M, int N, int K, int group_size,
+                                 void *stream);
+
+/* The same grouped by expert over ragged rows: w [G, N, K/2], scales and zeros
+ * [G, K/group_size, N], m_offsets [G + 1] as for the ragged BF16 products (rows
+ * outside them are not written; experts without rows read nothing).
+ * 1 <= G <= 1024. */
+DG_API dg_status_t dg_m_grouped_w4_gemv_nt_ragged(const void *x, const uint8_t *w,
+                                                  const void *scales, const uint8_t *zeros, void *d,
+                                                  const int32_t *m_offsets, int M_total, int N,
+                                                  int K, int G, int group_size, void *stream);
+
+/*
  * Per-token 1x128 activation quantiser (page 2 "技术特性": fine-grained
  * dynamic scaling; page 3 "核心功能": block-wise scaling): produces the A
  * operand and sfa of the GEMMs above from BF16 activations.  For each row m

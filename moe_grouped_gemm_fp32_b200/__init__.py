@@ -1,6 +1,8 @@
 """Python binding of the B200 GEMM library (``_dg.so``): FP8 block-scaled NT
 GEMMs (dense, M-grouped contiguous and masked, K-grouped), the fused expert
-FFN, BF16 GEMMs in the same layouts, and the per-token 1x128 quantiser.
+FFN, BF16 GEMMs in the same layouts, ragged grouped BF16 products (forward and
+both gradients), products of a few rows with 4-bit weights, and the per-token
+1x128 quantiser.
 
 Argument marshalling only: every function below checks dtypes and shapes of
 torch CUDA tensors, reads their raw pointers and calls the C function of the
@@ -69,6 +71,11 @@ def lib() -> ctypes.CDLL:
     L.dg_bf16_gemm_nt.argtypes = [P, P, P, I, I, I, P]
     L.dg_m_grouped_bf16_gemm_nt_contiguous.argtypes = [P, P, P, P, I, I, I, I, P]
     L.dg_m_grouped_bf16_gemm_nt_masked.argtypes = [P, P, P, P, I, I, I, I, P]
+    L.dg_m_grouped_bf16_gemm_nt_ragged.argtypes = [P, P, P, P, I, I, I, I, P]
+    L.dg_m_grouped_bf16_gemm_nn_ragged.argtypes = [P, P, P, P, I, I, I, I, P]
+    L.dg_k_grouped_bf16_gemm_tn_ragged.argtypes = [P, P, P, I, P, I, I, I, I, I, P]
+    L.dg_w4_gemv_nt.argtypes = [P, P, P, P, P, I, I, I, I, P]
+    L.dg_m_grouped_w4_gemv_nt_ragged.argtypes = [P, P, P, P, P, P, I, I, I, I, I, P]
     L.dg_per_token_cast_to_fp8.argtypes = [P, P, P, I, I, I, P]
     L.dg_per_token_cast_to_fp8_masked.argtypes = [P, P, P, I, P, I, I, I, P]
     for f in ("dg_fp8_gemm_nt", "dg_m_grouped_fp8_gemm_nt_contiguous",
@@ -76,6 +83,9 @@ def lib() -> ctypes.CDLL:
               "dg_m_grouped_fp8_gemm_swiglu_quant_contiguous", "dg_m_grouped_fp8_ffn_contiguous",
               "dg_bf16_gemm_nt", "dg_m_grouped_bf16_gemm_nt_contiguous",
               "dg_m_grouped_bf16_gemm_nt_masked",
+              "dg_m_grouped_bf16_gemm_nt_ragged", "dg_m_grouped_bf16_gemm_nn_ragged",
+              "dg_k_grouped_bf16_gemm_tn_ragged",
+              "dg_w4_gemv_nt", "dg_m_grouped_w4_gemv_nt_ragged",
               "dg_per_token_cast_to_fp8",
               "dg_per_token_cast_to_fp8_masked"):
         getattr(L, f).restype = I
@@ -377,6 +387,115 @@ def dg_m_grouped_bf16_gemm_nt_masked(a, b, d, masked_m, stream=None):
     _call("dg_m_grouped_bf16_gemm_nt_masked", lib().dg_m_grouped_bf16_gemm_nt_masked,
           (a, b, d, masked_m), stream, *ptrs, G, Mmax, N, K)
     return d
+
+# --------------------------------------------------------------------------- ragged BF16 products
+def dg_m_grouped_bf16_gemm_nt_ragged(a, b, d, m_offsets, stream=None):
+    """Ragged M-grouped BF16 product (forward): a [M_total,K], b [G,N,K],
+    d [M_total,N]; m_offsets int32 [G+1] (device), expert g owning the rows
+    m_offsets[g] <= m < m_offsets[g+1].  Rows outside the offsets are not
+    written."""
+    import torch
+    ptrs = (_req(a, torch.bfloat16, "a", 2), _req(b, torch.bfloat16, "b", 3),
+            _req(d, torch.bfloat16, "d", 2), _req(m_offsets, torch.int32, "m_offsets", 1))
+    M_total, K = a.shape
+    G, N, _ = b.shape
+    _shape(b, (G, N, K), "b")
+    _shape(d, (M_total, N), "d")
+    _shape(m_offsets, (G + 1,), "m_offsets")
+    _call("dg_m_grouped_bf16_gemm_nt_ragged", lib().dg_m_grouped_bf16_gemm_nt_ragged,
+          (a, b, d, m_offsets), stream, *ptrs, M_total, N, K, G)
+    return d
+
+
+def dg_m_grouped_bf16_gemm_nn_ragged(a, b, d, m_offsets, stream=None):
+    """Ragged M-grouped BF16 product with b [G,K,N] (input gradient: a
+    [M_total,K] the output's gradient, b the forward's weights as they lie),
+    d [M_total,N]; m_offsets as in the forward."""
+    import torch
+    ptrs = (_req(a, torch.bfloat16, "a", 2), _req(b, torch.bfloat16, "b", 3),
+            _req(d, torch.bfloat16, "d", 2), _req(m_offsets, torch.int32, "m_offsets", 1))
+    M_total, K = a.shape
+    G, _, N = b.shape
+    _shape(b, (G, K, N), "b")
+    _shape(d, (M_total, N), "d")
+    _shape(m_offsets, (G + 1,), "m_offsets")
+    _call("dg_m_grouped_bf16_gemm_nn_ragged", lib().dg_m_grouped_bf16_gemm_nn_ragged,
+          (a, b, d, m_offsets), stream, *ptrs, M_total, N, K, G)
+    return d
+
+
+def dg_k_grouped_bf16_gemm_tn_ragged(a, b, d, k_offsets, accumulate=False, stream=None):
+    """Ragged K-grouped BF16 product (weight gradient): d [G,M,N] (float32 or
+    bfloat16) = sum over expert g's tokens k of a [K_total,M] x b [K_total,N];
+    k_offsets int32 [G+1] (device).  accumulate adds to what d holds."""
+    import torch
+    if not isinstance(d, torch.Tensor) or d.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("d must be a float32 or bfloat16 CUDA tensor")
+    ptrs = (_req(a, torch.bfloat16, "a", 2), _req(b, torch.bfloat16, "b", 2),
+            _req(d, d.dtype, "d", 3), _req(k_offsets, torch.int32, "k_offsets", 1))
+    K_total, M = a.shape
+    N = b.shape[1]
+    G = k_offsets.shape[0] - 1
+    _shape(b, (K_total, N), "b")
+    _shape(d, (G, M, N), "d")
+    _call("dg_k_grouped_bf16_gemm_tn_ragged", lib().dg_k_grouped_bf16_gemm_tn_ragged,
+          (a, b, d, k_offsets), stream, ptrs[0], ptrs[1], ptrs[2], int(d.dtype == torch.float32),
+          ptrs[3], G, M, N, K_total, int(bool(accumulate)))
+    return d
+
+
+# --------------------------------------------------------------------------- 4-bit weights
+def _w4_group_size(K, scales):
+    """k per scale group, from the scales' shape (left to the C call's checks if it does not divide)."""
+    groups = scales.shape[-2]
+    return K // groups if groups > 0 and K % groups == 0 else 0
+
+
+def dg_w4_gemv_nt(x, w, scales, d, zeros=None, stream=None):
+    """d [M,N] (bfloat16) = x [M,K] (bfloat16) times 4-bit weights: w uint8
+    [N,K/2] (low four bits: even k), scales bfloat16 [K/group_size,N], zeros
+    uint8 of the scales' shape or None (8); weight = scale * (code - zero).  For
+    few rows.  w, scales and zeros may carry a leading dimension of 1."""
+    import torch
+    ptrs = (_req(x, torch.bfloat16, "x", 2), _req(w, torch.uint8, "w", (2, 3)),
+            _req(scales, torch.bfloat16, "scales", (2, 3)), _req(d, torch.bfloat16, "d", 2))
+    zp = None if zeros is None else _req(zeros, torch.uint8, "zeros", (2, 3))
+    M, K = x.shape
+    N = w.shape[-2]
+    groups = scales.shape[-2]
+    _shape(w, (1,) * (w.dim() - 2) + (N, K // 2 if K % 2 == 0 else -1), "w")
+    _shape(scales, (1,) * (scales.dim() - 2) + (groups, N), "scales")
+    if zeros is not None:
+        _shape(zeros, (1,) * (zeros.dim() - 2) + (groups, N), "zeros")
+    _shape(d, (M, N), "d")
+    _call("dg_w4_gemv_nt", lib().dg_w4_gemv_nt, (x, w, scales, d) + (() if zeros is None else (zeros,)), stream,
+          ptrs[0], ptrs[1], ptrs[2], zp, ptrs[3], M, N, K, _w4_group_size(K, scales))
+    return d
+
+
+def dg_m_grouped_w4_gemv_nt_ragged(x, w, scales, d, m_offsets, zeros=None, stream=None):
+    """The 4-bit product grouped by expert over ragged rows: x [M_total,K], w
+    uint8 [G,N,K/2], scales bfloat16 [G,K/group_size,N], zeros uint8 of the
+    scales' shape or None, d [M_total,N]; m_offsets int32 [G+1] (device)."""
+    import torch
+    ptrs = (_req(x, torch.bfloat16, "x", 2), _req(w, torch.uint8, "w", 3),
+            _req(scales, torch.bfloat16, "scales", 3), _req(d, torch.bfloat16, "d", 2),
+            _req(m_offsets, torch.int32, "m_offsets", 1))
+    zp = None if zeros is None else _req(zeros, torch.uint8, "zeros", 3)
+    M_total, K = x.shape
+    G, N, _ = w.shape
+    groups = scales.shape[-2]
+    _shape(w, (G, N, K // 2 if K % 2 == 0 else -1), "w")
+    _shape(scales, (G, groups, N), "scales")
+    if zeros is not None:
+        _shape(zeros, (G, groups, N), "zeros")
+    _shape(d, (M_total, N), "d")
+    _shape(m_offsets, (G + 1,), "m_offsets")
+    _call("dg_m_grouped_w4_gemv_nt_ragged", lib().dg_m_grouped_w4_gemv_nt_ragged,
+          (x, w, scales, d, m_offsets) + (() if zeros is None else (zeros,)), stream,
+          ptrs[0], ptrs[1], ptrs[2], zp, ptrs[3], ptrs[4], M_total, N, K, G, _w4_group_size(K, scales))
+    return d
+
 
 # --------------------------------------------------------------------------- quantisers
 def dg_per_token_cast_to_fp8(x, q, sfa, stream=None):

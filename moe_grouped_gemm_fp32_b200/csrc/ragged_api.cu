@@ -1,0 +1,192 @@
+// ragged_api.cu -- host side of the ragged grouped BF16 products declared in
+// include/dg.h (dg_m_grouped_bf16_gemm_nt_ragged, dg_m_grouped_bf16_gemm_nn_ragged,
+// dg_k_grouped_bf16_gemm_tn_ragged): argument validation, TMA descriptors, tile
+// choice, launch.  Nothing here synchronises the host or allocates memory.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cstdio>
+
+#include "dg.h"
+#include "api_common.h"
+#include "ragged_kernel.cuh"
+
+namespace {
+using namespace dg_host;
+
+constexpr long long kMaxInt = (1LL << 31) - 1;
+
+// rows: the token buffer's; p, q: the two other sizes, both innermost somewhere
+dg_status_t check_ragged(const void *a, const void *b, const void *d, const int32_t *offsets, int rows, int p, int q,
+                         int G) {
+    if (!b || !offsets || (rows > 0 && (!a || !d))) return DG_ERR_INVALID_VALUE;
+    if (rows < 0 || p <= 0 || q <= 0 || G <= 0) return DG_ERR_INVALID_VALUE;
+    if (p % 8 != 0 || q % 8 != 0) return DG_ERR_UNSUPPORTED_SHAPE;        // 16-byte rows
+    if (G > dg::kMaxGroups || p > (1 << 30) || q > (1 << 30)) return DG_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned16(a) || !aligned16(b) || !aligned16(d)) return DG_ERR_MISALIGNED;
+    return DG_SUCCESS;
+}
+
+template <int kDir, int kBN, int kStages, int kCtaGroup, bool kF32>
+struct Launch {
+    using L = dg::RaggedSmem<kDir, kBN, kStages, kCtaGroup>;
+
+    static auto kernel() { return dg::ragged_gemm_kernel<kDir, kBN, kStages, kCtaGroup, kF32>; }
+
+    static void config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute *attr, int grid, cudaStream_t stream) {
+        cfg = {};
+        cfg.gridDim = dim3(grid, 1, 1);
+        cfg.blockDim = dim3(dg::kRaggedThreads, 1, 1);
+        cfg.dynamicSmemBytes = L::kAlloc;
+        cfg.stream = stream;
+        cfg.attrs = attr;
+        cfg.numAttrs = 0;
+        if (kCtaGroup > 1) {
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = kCtaGroup;
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cfg.numAttrs = 1;
+        }
+    }
+
+    // One-time set-up per device; resident tiles (CTAs or CTA pairs) in *units.
+    // Idempotent: the atomic keeps racing first calls defined.
+    static dg_status_t setup(const DeviceInfo *info, int *units) {
+        static std::atomic<int> cache[kMaxDevices] = {};
+        int dev = 0;
+        cudaGetDevice(&dev);
+        if ((*units = cache[dev].load(std::memory_order_acquire)) > 0) return DG_SUCCESS;
+        cudaError_t e = cudaFuncSetAttribute(kernel(), cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(ragged smem)");
+        if (kF32 && kBN == 256) {
+            // the register hand-over between warpgroups adds up only for this launch size
+            cudaFuncAttributes fa;
+            if ((e = cudaFuncGetAttributes(&fa, kernel())) != cudaSuccess) return cuda_fail(e, "cudaFuncGetAttributes");
+            if (fa.numRegs != dg::kRegsLaunch) return cuda_fail(cudaErrorLaunchOutOfResources, "ragged kernel registers");
+        }
+        int n = info->num_sms;
+        if (kCtaGroup > 1) {
+            cudaLaunchConfig_t cfg;
+            cudaLaunchAttribute attr[1];
+            config(cfg, attr, kCtaGroup, nullptr);
+            if ((e = cudaOccupancyMaxActiveClusters(&n, kernel(), &cfg)) != cudaSuccess)
+                return cuda_fail(e, "cudaOccupancyMaxActiveClusters(ragged)");
+            if (n <= 0) return cuda_fail(cudaErrorLaunchOutOfResources, "ragged CTA pairs");
+        }
+        *units = n;
+        cache[dev].store(n, std::memory_order_release);
+        return DG_SUCCESS;
+    }
+
+    // tiles: an upper bound of the tile count
+    static dg_status_t run(const CUtensorMap &ma, const CUtensorMap &mb, const dg::RaggedParams &p, long long tiles,
+                           const DeviceInfo *info, cudaStream_t stream) {
+        int units = 0;
+        dg_status_t st = setup(info, &units);
+        if (st != DG_SUCCESS) return st;
+        const int grid = kCtaGroup * static_cast<int>(tiles < units ? tiles : units);
+        if (verbose())
+            std::fprintf(stderr, "[dg] ragged dir=%d bn=%d stages=%d ctas/mma=%d f32=%d grid=%d smem=%d\n", kDir, kBN,
+                         kStages, kCtaGroup, kF32 ? 1 : 0, grid, L::kAlloc);
+        cudaLaunchConfig_t cfg;
+        cudaLaunchAttribute attr[1];
+        config(cfg, attr, grid, stream);
+        cudaError_t e = cudaLaunchKernelEx(&cfg, kernel(), ma, mb, p);
+        return e == cudaSuccess ? DG_SUCCESS : cuda_fail(e, "ragged_gemm_kernel launch");
+    }
+};
+
+long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
+
+dg::RaggedParams ragged_params(void *d, const int32_t *offsets, int T, int M, int N, int K, int G, int accumulate,
+                               const DeviceInfo *info) {
+    dg::RaggedParams p = {};
+    p.d = d;
+    p.offsets = offsets;
+    p.status = info->status;
+    p.timeout_cycles = timeout_cycles();
+    p.T = T;
+    p.M = M;
+    p.N = N;
+    p.K = K;
+    p.G = G;
+    p.accumulate = accumulate;
+    p.debug_flags = debug_flags();
+    return p;
+}
+
+// Forward and input gradient: a [T, K], b [G, N, K] (kNT) or [G, K, N] (kNN).
+template <int kDir>
+dg_status_t m_grouped(const void *a, const void *b, void *d, const int32_t *offsets, int T, int N, int K, int G,
+                      cudaStream_t stream) {
+    dg_status_t st = check_ragged(a, b, d, offsets, T, N, K, G);
+    if (st != DG_SUCCESS) return st;
+    const int used = T < G ? T : G;              // experts that can have a row
+    if ((ceil_div(T, 128) + used) * ceil_div(N, 64) > kMaxInt) return DG_ERR_UNSUPPORTED_SHAPE;
+    const DeviceInfo *info = nullptr;
+    if ((st = device_info(&info)) != DG_SUCCESS) return st;
+    if (T == 0) return DG_SUCCESS;
+    const dg::RaggedParams p = ragged_params(d, offsets, T, 0, N, K, G, 0, info);
+    // 256-row CTA pairs where an expert has 128 rows or more on average
+    const bool pair = N > 128 && T >= 256 && T / used >= 128;
+    const int bn = pair ? 256 : ceil_div(N, 128) * used >= info->num_sms ? 128 : 64;
+    CUtensorMap ma, mb;
+    if ((st = make_kmajor_map(&ma, a, 2, K, T, 1, pair ? 128 : 32)) != DG_SUCCESS) return st;
+    st = kDir == dg::kNT ? make_kmajor_map(&mb, b, 2, K, N, G, pair ? bn / 2 : bn)
+                         : make_kmajor_map(&mb, b, 2, N, K, G, dg::kRaggedBlockK);
+    if (st != DG_SUCCESS) return st;
+    const long long tiles = (ceil_div(T, pair ? 256 : 128) + used) * ceil_div(N, bn);
+    if (pair) return Launch<kDir, 256, 6, 2, false>::run(ma, mb, p, tiles, info, stream);
+    if (bn == 128) return Launch<kDir, 128, 6, 1, false>::run(ma, mb, p, tiles, info, stream);
+    return Launch<kDir, 64, 8, 1, false>::run(ma, mb, p, tiles, info, stream);
+}
+
+template <bool kF32>
+dg_status_t k_grouped(const void *a, const void *b, const dg::RaggedParams &p, const DeviceInfo *info,
+                      cudaStream_t stream) {
+    CUtensorMap ma, mb;
+    dg_status_t st = make_kmajor_map(&ma, a, 2, p.M, p.T, 1, dg::kRaggedBlockK);
+    if (st != DG_SUCCESS) return st;
+    if ((st = make_kmajor_map(&mb, b, 2, p.N, p.T, 1, dg::kRaggedBlockK)) != DG_SUCCESS) return st;
+    if (p.M > 128 && p.N > 128)
+        return Launch<dg::kTN, 256, 6, 2, kF32>::run(ma, mb, p, p.G * ceil_div(p.M, 256) * ceil_div(p.N, 256), info, stream);
+    return Launch<dg::kTN, 128, 6, 1, kF32>::run(ma, mb, p, p.G * ceil_div(p.M, 128) * ceil_div(p.N, 128), info, stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+dg_status_t dg_m_grouped_bf16_gemm_nt_ragged(const void *a, const void *b, void *d, const int32_t *m_offsets,
+                                             int M_total, int N, int K, int G, void *stream) {
+    return m_grouped<dg::kNT>(a, b, d, m_offsets, M_total, N, K, G, static_cast<cudaStream_t>(stream));
+}
+
+dg_status_t dg_m_grouped_bf16_gemm_nn_ragged(const void *a, const void *b, void *d, const int32_t *m_offsets,
+                                             int M_total, int N, int K, int G, void *stream) {
+    return m_grouped<dg::kNN>(a, b, d, m_offsets, M_total, N, K, G, static_cast<cudaStream_t>(stream));
+}
+
+dg_status_t dg_k_grouped_bf16_gemm_tn_ragged(const void *a, const void *b, void *d, int d_is_fp32,
+                                             const int32_t *k_offsets, int G, int M, int N, int K_total,
+                                             int accumulate, void *stream) {
+    if (!d) return DG_ERR_INVALID_VALUE;
+    dg_status_t st = check_ragged(a, K_total > 0 ? b : d, d, k_offsets, K_total, M, N, G);
+    if (st != DG_SUCCESS) return st;
+    if (G * ceil_div(M, 128) * ceil_div(N, 128) > kMaxInt) return DG_ERR_UNSUPPORTED_SHAPE;
+    const DeviceInfo *info = nullptr;
+    if ((st = device_info(&info)) != DG_SUCCESS) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (K_total == 0) {                           // no tokens: zeros, or nothing to add
+        if (accumulate) return DG_SUCCESS;
+        const size_t bytes = static_cast<size_t>(G) * M * N * (d_is_fp32 ? 4 : 2);
+        cudaError_t e = cudaMemsetAsync(d, 0, bytes, s);
+        return e == cudaSuccess ? DG_SUCCESS : cuda_fail(e, "cudaMemsetAsync");
+    }
+    const dg::RaggedParams p = ragged_params(d, k_offsets, K_total, M, N, 0, G, accumulate ? 1 : 0, info);
+    return d_is_fp32 ? k_grouped<true>(a, b, p, info, s) : k_grouped<false>(a, b, p, info, s);
+}
+
+}  // extern "C"

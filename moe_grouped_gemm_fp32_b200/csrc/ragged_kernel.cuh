@@ -1,0 +1,578 @@
+// ragged_kernel.cuh -- the sm_100a kernel of the ragged grouped BF16 products:
+// experts own runs of a token buffer given by offsets on the device, with no
+// padding between them.  Three directions share one kernel:
+//
+//   kNT  D[r,n]    = sum_k A[r,k] * B[g(r)][n,k]        forward
+//   kNN  D[r,n]    = sum_k A[r,k] * B[g(r)][k,n]        input gradient
+//   kTN  D[g][m,n] = sum_{r in g} A[r,m] * B[r,n]       weight gradient
+//
+// Operands.  tcgen05.mma reads either operand K-major (the reduced index
+// innermost) or MN-major; both come straight from the caller's layout by TMA
+// with 128-byte swizzle, nothing is transposed in memory:
+//   K-major   box {64 K, rows}: one 128-byte line per row (kNT: A and B, kNN: A)
+//   MN-major  boxes {64 M or N, 64 K}: one 128-byte line per reduced index, 64
+//             columns wide; 8192 bytes between boxes, 1024 bytes between
+//             groups of 8 reduced indices (kNN: B, kTN: A and B)
+//
+// Ragged edges.
+//   kNT, kNN: a tile's token rows start at the expert's offset (TMA row
+//     coordinates need no alignment) and may run past its end: those rows are
+//     computed from the neighbour's tokens and not stored.  Rows of the product
+//     do not mix, so a NaN there stays there.
+//   kTN: the last block of 64 tokens of an expert may run into the next one's.
+//     Its MMAs stop at the last started group of 16 tokens, and the rows
+//     between the expert's end and that group's end are zeroed in shared
+//     memory, in both operands (0 * NaN would be NaN), by a warp of its own:
+//     the block's loads complete on a barrier of that warp, which clears the
+//     rows and only then hands the stage to the MMA warp.  The block comes last,
+//     so the MMAs of the blocks before it run meanwhile.
+//
+// Roles: warp 0 producer (TMA), warp 1 TMEM and MMA issue, warp 2 clears ragged
+// token rows (kTN), warps 4..11 epilogue: warp w drains TMEM lanes 32 (w % 4),
+// columns of half (w - 4) / 4.  Persistent; two accumulators in rotation, so
+// the next tile's MMAs overlap this tile's stores.
+//
+// CTA pairs (kCtaGroup == 2): 256 x kBN tiles, each CTA stages its 128 rows of
+// A and half of B's columns.  Single CTAs take over where experts have few
+// rows: there A comes in boxes of 32 rows, only those that the expert has, so
+// that weight bytes, not token tiles, fill the memory pipeline.
+//
+// Precision.  The tensor core's FP32 accumulator truncates: measured against 64
+// bits, a sum of 8192 products loses 9e-6 (relative, 2-norm) and 32768 products
+// 1.9e-5, where rounded FP32 sums lose 1e-6 and 2.3e-6.  A BF16 result rounds
+// at 2^-9 and does not see it.  An FP32 weight gradient does, so it is summed
+// in two levels: every kSegBlocks K-blocks (512 tokens, 5e-7) the accumulator
+// is read out and added, rounded, to FP32 registers of the epilogue warps.
+//
+// Every wait is bounded (BoundedWait).
+#pragma once
+
+#include "gemm_kernel.cuh"
+
+namespace dg {
+
+enum RaggedDir : int { kNT = 0, kNN = 1, kTN = 2 };
+
+constexpr int kRaggedThreads = 384;
+constexpr int kRaggedBlockK = 64;
+constexpr int kRaggedBand = 8;        // row blocks per L2 raster band
+constexpr int kSegBlocks = 8;         // K-blocks per accumulator segment, FP32 weight gradient
+constexpr unsigned kSiteBadOffsets = 12, kSiteTailRows = 13;
+
+struct RaggedParams {
+    void *d;
+    const int32_t *offsets;   // [G + 1]
+    unsigned *status;
+    long long timeout_cycles;
+    int T;                    // rows of the token buffer
+    int M, N, K;              // kTN: output rows M; kNT, kNN: reduced size K
+    int G;
+    int accumulate;           // kTN: add to d
+    int debug_flags;
+};
+
+template <int kDir, int kBN, int kStages, int kCtaGroup>
+struct RaggedSmem {
+    static constexpr int kABytes = kTileX * 128;
+    static constexpr int kBCols = kBN / kCtaGroup;            // this CTA's columns of B
+    static constexpr int kBBytes = kBCols * 128;
+    static constexpr int kStageBytes = kABytes + kBBytes;
+    static constexpr int kAccBufs = 2;
+    static constexpr int kBarOffset = kStages * kStageBytes;
+    static constexpr int kNumBars = 3 * kStages + 2 * kAccBufs + 1;
+    static constexpr int kMiscOffset = kBarOffset + kNumBars * 8;   // tmem addr, abort flag
+    static constexpr int kOffsOffset = (kMiscOffset + 16 + 15) / 16 * 16;
+    static constexpr int kPrefixOffset = kOffsOffset + (kMaxGroups + 1) * 4;
+    static constexpr int kUsed = kPrefixOffset + (kMaxGroups + 1) * 4;
+    static constexpr int kAlloc = (kUsed + 1024 > kMinSmem) ? kUsed + 1024 : kMinSmem;
+    static constexpr int kTmemCols = kAccBufs * kBN <= 128 ? 128 : kAccBufs * kBN <= 256 ? 256 : 512;
+    static_assert(kBN == 64 || kBN == 128 || kBN == 256, "tile N");
+    static_assert(kBCols % 64 == 0, "MN-major boxes are 64 columns wide");
+    static_assert(kAlloc <= 227 * 1024, "shared memory budget");
+};
+
+// MN-major, 128-byte swizzle: boxes of 64 columns by 64 reduced indices, 8192
+// bytes apart (leading offset); 1024 bytes between groups of 8 reduced indices.
+__device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t saddr) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr & 0x3FFFF) >> 4);
+    d |= static_cast<uint64_t>(8192 >> 4) << 16;
+    d |= static_cast<uint64_t>(1024 >> 4) << 32;
+    d |= static_cast<uint64_t>(1) << 46;
+    d |= static_cast<uint64_t>(2) << 61;
+    return d;
+}
+
+// kind::f16, D = F32, A = B = BF16; bits 15 and 16 mark MN-major A and B.
+__host__ __device__ constexpr uint32_t ragged_idesc(int m, int n, bool a_mn, bool b_mn) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) |
+           (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+struct RaggedTile {
+    int g;
+    int row0;      // kNT, kNN: first token row of the tile (in the buffer); kTN: first output row
+    int row_end;   // exclusive bound of its valid rows
+    int n0;
+    int num_kb;    // K-blocks of 64
+    int tail;      // kTN: tokens in the last K-block (1..64), 64 elsewhere
+};
+
+template <int kDir, int kBN, int kCtaGroup>
+struct RaggedMap {
+    static constexpr int kRows = kTileX * kCtaGroup;
+
+    __device__ static int row_blocks(const RaggedParams &p, const int *offs, int g) {
+        const int rows = kDir == kTN ? p.M : offs[g + 1] - offs[g];
+        return (rows + kRows - 1) / kRows;
+    }
+    __device__ static int count(const RaggedParams &p, const int *prefix) { return prefix[p.G]; }
+
+    __device__ static void decode(int t, const RaggedParams &p, const int *offs, const int *prefix,
+                                  RaggedTile &tl) {
+        int lo = 0, hi = p.G - 1;                     // last g with prefix[g] <= t
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (prefix[mid] <= t) lo = mid; else hi = mid - 1;
+        }
+        const int g = lo, local = t - prefix[g];
+        const int nb = (p.N + kBN - 1) / kBN;
+        const int rb = row_blocks(p, offs, g);
+        const int per_band = kRaggedBand * nb;
+        const int band = local / per_band;
+        const int width = min(kRaggedBand, rb - band * kRaggedBand);
+        const int in_band = local - band * per_band;
+        const int row = (band * kRaggedBand + in_band % width) * kRows;
+        tl.g = g;
+        tl.n0 = in_band / width * kBN;
+        const int tokens = offs[g + 1] - offs[g];
+        if (kDir == kTN) {
+            tl.row0 = row;
+            tl.row_end = p.M;
+            tl.num_kb = (tokens + kRaggedBlockK - 1) / kRaggedBlockK;
+            tl.tail = tokens - (tl.num_kb - 1) * kRaggedBlockK;
+        } else {
+            tl.row0 = offs[g] + row;
+            tl.row_end = offs[g + 1];
+            tl.num_kb = (p.K + kRaggedBlockK - 1) / kRaggedBlockK;
+            tl.tail = kRaggedBlockK;
+        }
+    }
+};
+
+__device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// Eight consecutive columns of one output row, 16-byte aligned (32 for FP32).
+template <bool kF32>
+__device__ __forceinline__ void store8(void *d, size_t index, const float *v, bool accumulate) {
+    if constexpr (kF32) {
+        float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(d) + index);
+        float4 a = make_float4(v[0], v[1], v[2], v[3]), b = make_float4(v[4], v[5], v[6], v[7]);
+        if (accumulate) {
+            const float4 x = o[0], y = o[1];
+            a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
+            b.x += y.x; b.y += y.y; b.z += y.z; b.w += y.w;
+        }
+        o[0] = a;
+        o[1] = b;
+    } else {
+        uint4 *o = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(d) + index);
+        float s[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[j] = v[j];
+        if (accumulate) {                       // BF16 is widened exactly, added in FP32, rounded once
+            const uint4 x = *o;
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                s[2 * j] += __uint_as_float(w[j] << 16);
+                s[2 * j + 1] += __uint_as_float(w[j] & 0xFFFF0000u);
+            }
+        }
+        *o = make_uint4(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]), pack_bf16x2(s[4], s[5]),
+                        pack_bf16x2(s[6], s[7]));
+    }
+}
+
+// tm_a, tm_b: see the operand table above (kNT, kNN single-CTA: A boxes of 32 rows).
+template <int kDir, int kBN, int kStages, int kCtaGroup, bool kF32>
+__global__ void __launch_bounds__(kRaggedThreads, 1)
+ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                   const RaggedParams p) {
+    using L = RaggedSmem<kDir, kBN, kStages, kCtaGroup>;
+    using TM = RaggedMap<kDir, kBN, kCtaGroup>;
+    static_assert(!kF32 || kDir == kTN, "FP32 output: weight gradient");
+    constexpr bool kPair = kCtaGroup == 2;
+    constexpr bool kAMn = kDir == kTN, kBMn = kDir != kNT;
+    constexpr int kAccBufs = L::kAccBufs;
+    constexpr int kEpiWarp0 = 4;
+    constexpr int kHalf = kBN / 2;                 // columns per epilogue warp
+    constexpr bool kPromote = kF32;                // two-level sums
+    constexpr bool kRebalance = kPromote && kHalf >= 128;
+
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const uint32_t s_base = ptx::smem_u32(smem);
+    const uint32_t bar_base = s_base + L::kBarOffset;
+    auto full_bar = [&](int s) { return bar_base + 8u * s; };
+    auto empty_bar = [&](int s) { return bar_base + 8u * (kStages + s); };
+    auto tail_bar = [&](int s) { return bar_base + 8u * (2 * kStages + s); };
+    auto tfull_bar = [&](int b) { return bar_base + 8u * (3 * kStages + b); };
+    auto tempty_bar = [&](int b) { return bar_base + 8u * (3 * kStages + kAccBufs + b); };
+    const uint32_t mma_done_bar = bar_base + 8u * (3 * kStages + 2 * kAccBufs);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kMiscOffset);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kMiscOffset + 4);
+    int *offs = reinterpret_cast<int *>(smem + L::kOffsOffset);
+    int *prefix = reinterpret_cast<int *>(smem + L::kPrefixOffset);
+
+    const int warp = threadIdx.x / 32;
+    const int lane = threadIdx.x % 32;
+    const BoundedWait wait{abort_flag, p.status, p.timeout_cycles};
+    const int pair_rank = kPair ? static_cast<int>(ptx::cluster_rank() & 1u) : 0;
+    const bool mma_cta = pair_rank == 0;
+    auto leader_addr = [&](uint32_t local) { return kPair ? ptx::map_cluster(local, 0) : local; };
+
+    if (threadIdx.x == 0) {
+        ptx::prefetch_tmap(&tm_a);
+        ptx::prefetch_tmap(&tm_b);
+        for (int i = 0; i < kStages; ++i) {
+            // kTN: one arrival per CTA (its producer, or its row-clearing warp)
+            ptx::mbar_init(full_bar(i), kDir == kTN ? kCtaGroup : 1);
+            ptx::mbar_init(empty_bar(i), 1);
+            ptx::mbar_init(tail_bar(i), 1);
+        }
+        for (int b = 0; b < kAccBufs; ++b) {
+            ptx::mbar_init(tfull_bar(b), 1);
+            ptx::mbar_init(tempty_bar(b), 8 * kCtaGroup);   // one arrival per epilogue warp of the pair
+        }
+        ptx::mbar_init(mma_done_bar, 1);
+        *abort_flag = 0;
+        ptx::fence_mbar_init();
+    }
+    if (warp == kEpiWarp0) {
+        // offsets as the tiles use them: clamped to [0, T] and made non-decreasing
+        int run = 0;
+        for (int base = 0; base <= p.G; base += 32) {
+            const int i = base + lane;
+            const int raw = i <= p.G ? __ldg(p.offsets + i) : 0;
+            int v = min(max(raw, 0), p.T);
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v = max(v, u);
+            }
+            v = max(v, run);
+            if (i <= p.G) {
+                offs[i] = v;
+                if (v != raw) record_status(p.status, kStatusInvalid, kSiteBadOffsets);
+            }
+            run = __shfl_sync(0xffffffffu, v, 31);
+        }
+        __syncwarp();
+        // exclusive prefix of tiles per expert
+        const int nb = (p.N + kBN - 1) / kBN;
+        int carry = 0;
+        for (int base = 0; base < p.G; base += 32) {
+            const int g = base + lane;
+            const int tiles = g < p.G ? TM::row_blocks(p, offs, g) * nb : 0;
+            int incl = tiles;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += u;
+            }
+            if (g < p.G) prefix[g] = carry + incl - tiles;
+            carry += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        if (lane == 0) prefix[p.G] = carry;
+    }
+    if (warp == 1) {
+        if constexpr (kPair) {
+            ptx::tmem_alloc_pair(ptx::smem_u32(tmem_slot), L::kTmemCols);
+            ptx::tmem_relinquish_pair();
+        } else {
+            ptx::tmem_alloc(ptx::smem_u32(tmem_slot), L::kTmemCols);
+            ptx::tmem_relinquish();
+        }
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    if constexpr (kPair) ptx::cluster_sync_all();   // the peer's barriers exist before any remote use
+    ptx::tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+
+    const int num_tiles = TM::count(p, prefix);
+    const int t_first = static_cast<int>(blockIdx.x) / kCtaGroup;
+    const int t_step = static_cast<int>(gridDim.x) / kCtaGroup;
+
+    if (warp < kEpiWarp0) {
+        if constexpr (kRebalance) ptx::regs_dec<kRegsIssue>();
+        if (warp == 0) {
+            // ======================================================== producer
+            if (ptx::elect_one()) {
+                int stage = 0;
+                uint32_t phase = 0, tail_phase = 0, tail_armed = 0;   // a bit per stage
+                long long issued = 0;
+                bool ok = (p.debug_flags & kDebugProducerIdle) == 0;
+                for (int t = t_first; ok && t < num_tiles; t += t_step) {
+                    RaggedTile tl;
+                    TM::decode(t, p, offs, prefix, tl);
+                    // kNT, kNN: rows of A that this CTA loads, in boxes of 32 (single CTAs) or 128
+                    const int a_boxes = (kDir != kTN && !kPair) ? (min(tl.row_end - tl.row0, kTileX) + 31) / 32 : 0;
+                    const uint32_t bytes = (kDir != kTN && !kPair) ? a_boxes * 4096u + L::kBBytes
+                                                                   : static_cast<uint32_t>(L::kStageBytes);
+                    const int nb0 = tl.n0 + pair_rank * L::kBCols;
+                    for (int kb = 0; kb < tl.num_kb; ++kb) {
+                        if (!wait(empty_bar(stage), phase ^ 1u, kSiteProducerEmpty)) { ok = false; break; }
+                        const uint32_t sa = s_base + stage * L::kStageBytes;
+                        const uint32_t sb = sa + L::kABytes;
+                        const int k0 = kb * kRaggedBlockK;
+                        // the ragged last block of tokens goes through the row-clearing warp
+                        const bool clear = kDir == kTN && kb == tl.num_kb - 1 && (tl.tail & 15) != 0;
+                        uint32_t bar;
+                        if (clear) {
+                            bar = tail_bar(stage);
+                            ptx::mbar_arrive_expect_tx(bar, bytes);
+                            tail_armed |= 1u << stage;
+                            tail_phase ^= 1u << stage;
+                        } else if (kPair) {
+                            bar = leader_addr(full_bar(stage));
+                            if (mma_cta) ptx::mbar_arrive_expect_tx(full_bar(stage), 2u * bytes);
+                            else if (kDir == kTN) ptx::mbar_arrive_remote(bar);
+                        } else {
+                            bar = full_bar(stage);
+                            ptx::mbar_arrive_expect_tx(bar, bytes);
+                        }
+                        auto load = [&](uint32_t dst, const CUtensorMap *m, int c0, int c1, int c2) {
+                            if (kPair && !clear) ptx::tma_load_3d_pair(dst, m, bar, c0, c1, c2);
+                            else ptx::tma_load_3d(dst, m, bar, c0, c1, c2);
+                        };
+                        if constexpr (kDir == kTN) {
+                            const int tok = offs[tl.g] + k0;
+                            for (int i = 0; i < 2; ++i)
+                                load(sa + i * 8192u, &tm_a, tl.row0 + pair_rank * kTileX + 64 * i, tok, 0);
+                            for (int i = 0; i < L::kBCols / 64; ++i)
+                                load(sb + i * 8192u, &tm_b, nb0 + 64 * i, tok, 0);
+                        } else {
+                            if constexpr (kPair) {
+                                load(sa, &tm_a, k0, tl.row0 + pair_rank * kTileX, 0);
+                            } else {
+                                for (int i = 0; i < a_boxes; ++i)
+                                    load(sa + i * 4096u, &tm_a, k0, tl.row0 + 32 * i, 0);
+                            }
+                            if constexpr (kDir == kNT) {
+                                load(sb, &tm_b, k0, nb0, tl.g);
+                            } else {
+                                for (int i = 0; i < L::kBCols / 64; ++i)
+                                    load(sb + i * 8192u, &tm_b, nb0 + 64 * i, k0, tl.g);
+                            }
+                        }
+                        ++issued;
+                        if (++stage == kStages) { stage = 0; phase ^= 1u; }
+                    }
+                }
+                // never leave with TMA writes into shared memory in flight: the last
+                // blocks handed to the row-clearing warp, then the last stages.  A
+                // pair's second CTA cannot see its other bytes land; for it the final
+                // cluster barrier, reached after the MMA CTA consumed every stage (or
+                // ran out of time waiting for it), covers them.
+                auto drain = [&](uint32_t bar, uint32_t par) {
+                    const long long start = clock64();
+                    while (!ptx::mbar_try_wait(bar, par)) {
+                        if (clock64() - start > p.timeout_cycles) {
+                            record_status(p.status, kStatusTimeout, kSiteTeardownLoads);
+                            break;
+                        }
+                    }
+                };
+                for (int s = 0; s < kStages; ++s)
+                    if ((tail_armed >> s) & 1u) drain(tail_bar(s), ((tail_phase >> s) & 1u) ^ 1u);
+                const long long first = !mma_cta ? issued : (issued > kStages ? issued - kStages : 0);
+                for (long long i = first; i < issued; ++i)
+                    drain(full_bar(static_cast<int>(i % kStages)), static_cast<uint32_t>((i / kStages) & 1));
+            }
+            __syncwarp();
+        } else if (warp == 1) {
+            // ======================================================== MMA issuer
+            if (mma_cta && ptx::elect_one()) {
+                int stage = 0, buf = 0;
+                uint32_t phase = 0, tphase = 0;
+                bool ok = true;
+                const uint32_t idesc = ragged_idesc(kTileX * kCtaGroup, kBN, kAMn, kBMn);
+                constexpr uint32_t kStepA = kAMn ? 2048 >> 4 : 32 >> 4;   // 16 reduced indices
+                constexpr uint32_t kStepB = kBMn ? 2048 >> 4 : 32 >> 4;
+                for (int t = t_first; ok && t < num_tiles; t += t_step) {
+                    RaggedTile tl;
+                    TM::decode(t, p, offs, prefix, tl);
+                    const int seg = kPromote ? kSegBlocks : tl.num_kb;
+                    for (int kb0 = 0; ok && kb0 < tl.num_kb; kb0 += seg) {
+                        if (!wait(tempty_bar(buf), tphase ^ 1u, kSiteMmaTmemEmpty)) { ok = false; break; }
+                        ptx::tc_fence_after();
+                        const uint32_t dtm = tmem_base + static_cast<uint32_t>(buf * kBN);
+                        const int kb1 = min(kb0 + seg, tl.num_kb);
+                        for (int kb = kb0; kb < kb1; ++kb) {
+                            if (!wait(full_bar(stage), phase, kSiteMmaFull)) { ok = false; break; }
+                            const bool last = kDir == kTN && kb == tl.num_kb - 1;
+                            if (kDir == kTN && kPair && last) ptx::fence_acq_rel_cluster();   // the peer's cleared rows
+                            ptx::tc_fence_after();
+                            const uint32_t sa = s_base + stage * L::kStageBytes;
+                            const uint64_t da = kAMn ? sw128_mn_desc(sa) : sw128_desc(sa);
+                            const uint64_t db = kBMn ? sw128_mn_desc(sa + L::kABytes) : sw128_desc(sa + L::kABytes);
+                            const int steps = last ? (tl.tail + 15) / 16 : kRaggedBlockK / 16;
+#pragma unroll
+                            for (int k = 0; k < kRaggedBlockK / 16; ++k) {
+                                if (k < steps) {
+                                    const uint32_t acc = (kb > kb0 || k > 0) ? 1u : 0u;
+                                    if constexpr (kPair) ptx::mma_f16_pair(dtm, da + kStepA * k, db + kStepB * k, idesc, acc);
+                                    else ptx::mma_f16(dtm, da + kStepA * k, db + kStepB * k, idesc, acc);
+                                }
+                            }
+                            if constexpr (kPair) ptx::mma_commit_pair(empty_bar(stage), 0x3);
+                            else ptx::mma_commit(empty_bar(stage));
+                            if (++stage == kStages) { stage = 0; phase ^= 1u; }
+                        }
+                        if (!ok) break;
+                        if constexpr (kPair) ptx::mma_commit_pair(tfull_bar(buf), 0x3);
+                        else ptx::mma_commit(tfull_bar(buf));
+                        if (++buf == kAccBufs) { buf = 0; tphase ^= 1u; }
+                    }
+                }
+                // the commit is issued even when nothing ran, so every wait on it is uniform
+                if constexpr (kPair) ptx::mma_commit_pair(mma_done_bar, 0x3);
+                else ptx::mma_commit(mma_done_bar);
+            }
+            __syncwarp();
+        } else if (kDir == kTN && warp == 2) {
+            // ======================================================== clears ragged token rows
+            long long block = 0;                  // K-blocks of the tiles before
+            uint32_t tail_phase = 0;              // a bit per stage
+            for (int t = t_first; t < num_tiles; t += t_step) {
+                RaggedTile tl;
+                TM::decode(t, p, offs, prefix, tl);
+                block += tl.num_kb;
+                if (tl.num_kb == 0 || (tl.tail & 15) == 0) continue;
+                const int stage = static_cast<int>((block - 1) % kStages);
+                if (!wait(tail_bar(stage), (tail_phase >> stage) & 1u, kSiteTailRows)) break;
+                tail_phase ^= 1u << stage;
+                // rows tail .. next multiple of 16, one 128-byte line per box and row (the
+                // swizzle only permutes within a line)
+                const int rows = 16 - (tl.tail & 15);
+                constexpr int kBoxes = 2 + L::kBCols / 64;
+                uint8_t *base = smem + stage * L::kStageBytes + tl.tail * 128;
+                for (int i = lane; i < kBoxes * rows * 8; i += 32) {
+                    const int box = i / (rows * 8), at = i - box * rows * 8;
+                    *reinterpret_cast<uint4 *>(base + box * 8192 + at * 16) = make_uint4(0u, 0u, 0u, 0u);
+                }
+                ptx::fence_proxy_async_smem();    // the MMAs read through the async proxy
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive_cluster(leader_addr(full_bar(stage)));
+            }
+        }
+    } else {
+        // ============================================================ epilogue
+        if constexpr (kRebalance) ptx::regs_inc<kRegsPromo>();
+        const int quarter = warp & 3;
+        const int half = (warp - kEpiWarp0) >> 2;
+        const int lrow = pair_rank * kTileX + quarter * 32 + lane;
+        int buf = 0;
+        uint32_t tphase = 0;
+        bool ok = true;
+        auto release = [&]() {
+            // the accumulator is free for the MMA warp (on the MMA CTA's barrier)
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (kPair && !mma_cta) ptx::mbar_arrive_remote(leader_addr(tempty_bar(buf)));
+                else ptx::mbar_arrive(tempty_bar(buf));
+            }
+            if (++buf == kAccBufs) { buf = 0; tphase ^= 1u; }
+        };
+        for (int t = t_first; ok && t < num_tiles; t += t_step) {
+            RaggedTile tl;
+            TM::decode(t, p, offs, prefix, tl);
+            const int row = tl.row0 + lrow;
+            const bool row_ok = row < tl.row_end;
+            const size_t base = (kDir == kTN ? static_cast<size_t>(tl.g) * p.M + row : static_cast<size_t>(row)) *
+                                static_cast<size_t>(p.N);
+            const int c0 = tl.n0 + half * kHalf;
+            const bool add = kDir == kTN && p.accumulate;
+            if (tl.num_kb == 0) {                  // kTN, an expert without tokens
+                if (!add && row_ok) {
+                    const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                    for (int j = 0; j < kHalf; j += 8)
+                        if (c0 + j < p.N) store8<kF32>(p.d, base + c0 + j, zero, false);
+                }
+                continue;
+            }
+            if constexpr (kPromote) {
+                float acc[kHalf];
+#pragma unroll
+                for (int j = 0; j < kHalf; ++j) acc[j] = 0.f;
+                for (int kb0 = 0; kb0 < tl.num_kb; kb0 += kSegBlocks) {
+                    if (!wait(tfull_bar(buf), tphase, kSitePromoFull)) { ok = false; break; }
+                    ptx::tc_fence_after();
+                    const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
+                                           static_cast<uint32_t>(buf * kBN + half * kHalf);
+#pragma unroll
+                    for (int c = 0; c < kHalf; c += 16) {
+                        float v[16];
+                        ptx::tmem_ld16(taddr + c, v);
+                        ptx::tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) acc[c + j] += v[j];
+                    }
+                    release();
+                }
+                if (!ok) break;
+                if (row_ok) {
+#pragma unroll
+                    for (int j = 0; j < kHalf; j += 8)
+                        if (c0 + j < p.N) store8<kF32>(p.d, base + c0 + j, acc + j, add);
+                }
+            } else {
+                if (!wait(tfull_bar(buf), tphase, kSitePromoFull)) { ok = false; break; }
+                ptx::tc_fence_after();
+                const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
+                                       static_cast<uint32_t>(buf * kBN + half * kHalf);
+#pragma unroll 1
+                for (int c = 0; c < kHalf; c += 32) {
+                    float v[32];
+                    ptx::tmem_ld32p(taddr + c, v);
+                    ptx::tmem_wait_ld();
+                    if (row_ok) {
+#pragma unroll
+                        for (int j = 0; j < 32; j += 8)
+                            if (c0 + c + j < p.N) store8<kF32>(p.d, base + c0 + c + j, v + j, add);
+                    }
+                }
+                release();
+            }
+        }
+    }
+
+    // ---------------------------------------------------------------- teardown
+    if (warp == 1 && ptx::elect_one()) {
+        const long long start = clock64();
+        while (!ptx::mbar_try_wait(mma_done_bar, 0)) {
+            if (clock64() - start > p.timeout_cycles) {
+                record_status(p.status, kStatusTimeout, kSiteTeardownMma);
+                break;
+            }
+        }
+    }
+    __syncwarp();
+    ptx::tc_fence_before();
+    __syncthreads();
+    if constexpr (kPair) ptx::cluster_sync_all();   // no CTA leaves while its peer may touch its smem
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        if constexpr (kPair) ptx::tmem_dealloc_pair(tmem_base, L::kTmemCols);
+        else ptx::tmem_dealloc(tmem_base, L::kTmemCols);
+    }
+}
+
+}  // namespace dg
