@@ -328,8 +328,8 @@ DG_API dg_status_t dg_k_grouped_bf16_gemm_tn_ragged(const void *a, const void *b
  *   zeros  [K/group_size, N] uint8, 0..127, or NULL for 8 everywhere
  * q - z is exact and the scale is applied to the group's FP32 sum, so no weight
  * is rounded.  group_size 32, 64 or 128, K % group_size == 0, N % 8 == 0,
- * N <= 65535 * 128.  Any M: rows are taken up to 32 at a time and the weights
- * read once for each such run, so the call is meant for few.  M == 0 is a no-op
+ * N <= 65535 * 128.  Rows are taken up to 32 at a time and the weights
+ * read once for each such run, so the call is meant for few (M <= 65535 * 32).  M == 0 is a no-op
  * (x and d may be NULL).
  */
 DG_API dg_status_t dg_w4_gemv_nt(const void *x, const uint8_t *w, const void *scales,

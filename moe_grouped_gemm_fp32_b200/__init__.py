@@ -111,16 +111,32 @@ def _check(status: int, where: str):
         raise DGError(status, where, detail)
 
 
+_torch = None
+
+
+def _th():
+    """torch, imported at the first call: most of a small call's time is this
+    module's, so the checks below avoid what is slow in it (import statements,
+    torch.device and torch.cuda.Stream objects)."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
 def _stream_handle(stream) -> Optional[int]:
-    import torch
     if stream is None:
+        torch = _th()
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None:
+            return raw(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream
 
 
 def _req(t, dtype, name, ndim=None):
-    import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not isinstance(t, _th().Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
@@ -136,7 +152,10 @@ def _shape(t, want, name):
     entry is a size this call cannot know (left to the C call's own checks).
     The C functions receive only pointers and sizes, so a buffer smaller than
     its sizes imply must be caught here."""
-    got = tuple(t.shape)
+    got = t.shape
+    if got == want:
+        return
+    got = tuple(got)
     if len(got) != len(want) or any(w is not None and g != w for g, w in zip(got, want)):
         shown = tuple("*" if w is None else w for w in want)
         raise ValueError(f"{name} has shape {got}, expected {shown}")
@@ -156,14 +175,16 @@ def _call(where, fn, tensors, stream, *args):
     """Call ``fn(*args, stream_handle)`` and raise on a non-success status.
     The C library launches on the current CUDA device, so every tensor (and
     the stream, if given) must live on that device."""
-    import torch
-    devs = {t.device for t in tensors}
-    if len(devs) != 1:
-        raise ValueError(f"{where}: all tensors must be on one CUDA device, got {sorted(map(str, devs))}")
-    dev = devs.pop()
-    if dev.type == "cuda" and dev.index != torch.cuda.current_device():
-        raise ValueError(f"{where}: tensors are on {dev} but the current device is "
-                         f"cuda:{torch.cuda.current_device()} (select it with torch.cuda.device)")
+    dev = tensors[0].device
+    for t in tensors:
+        if t.device != dev:
+            raise ValueError(f"{where}: all tensors must be on one CUDA device, got "
+                             f"{sorted({str(x.device) for x in tensors})}")
+    if dev.type == "cuda":
+        current = _th().cuda.current_device()
+        if dev.index != current:
+            raise ValueError(f"{where}: tensors are on {dev} but the current device is "
+                             f"cuda:{current} (select it with torch.cuda.device)")
     if stream is not None and stream.device != dev:
         raise ValueError(f"{where}: stream is on {stream.device}, tensors on {dev}")
     _check(fn(*args, _stream_handle(stream)), where)
@@ -394,7 +415,7 @@ def dg_m_grouped_bf16_gemm_nt_ragged(a, b, d, m_offsets, stream=None):
     d [M_total,N]; m_offsets int32 [G+1] (device), expert g owning the rows
     m_offsets[g] <= m < m_offsets[g+1].  Rows outside the offsets are not
     written."""
-    import torch
+    torch = _th()
     ptrs = (_req(a, torch.bfloat16, "a", 2), _req(b, torch.bfloat16, "b", 3),
             _req(d, torch.bfloat16, "d", 2), _req(m_offsets, torch.int32, "m_offsets", 1))
     M_total, K = a.shape
@@ -411,7 +432,7 @@ def dg_m_grouped_bf16_gemm_nn_ragged(a, b, d, m_offsets, stream=None):
     """Ragged M-grouped BF16 product with b [G,K,N] (input gradient: a
     [M_total,K] the output's gradient, b the forward's weights as they lie),
     d [M_total,N]; m_offsets as in the forward."""
-    import torch
+    torch = _th()
     ptrs = (_req(a, torch.bfloat16, "a", 2), _req(b, torch.bfloat16, "b", 3),
             _req(d, torch.bfloat16, "d", 2), _req(m_offsets, torch.int32, "m_offsets", 1))
     M_total, K = a.shape
@@ -428,7 +449,7 @@ def dg_k_grouped_bf16_gemm_tn_ragged(a, b, d, k_offsets, accumulate=False, strea
     """Ragged K-grouped BF16 product (weight gradient): d [G,M,N] (float32 or
     bfloat16) = sum over expert g's tokens k of a [K_total,M] x b [K_total,N];
     k_offsets int32 [G+1] (device).  accumulate adds to what d holds."""
-    import torch
+    torch = _th()
     if not isinstance(d, torch.Tensor) or d.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError("d must be a float32 or bfloat16 CUDA tensor")
     ptrs = (_req(a, torch.bfloat16, "a", 2), _req(b, torch.bfloat16, "b", 2),
@@ -456,7 +477,7 @@ def dg_w4_gemv_nt(x, w, scales, d, zeros=None, stream=None):
     [N,K/2] (low four bits: even k), scales bfloat16 [K/group_size,N], zeros
     uint8 of the scales' shape or None (8); weight = scale * (code - zero).  For
     few rows.  w, scales and zeros may carry a leading dimension of 1."""
-    import torch
+    torch = _th()
     ptrs = (_req(x, torch.bfloat16, "x", 2), _req(w, torch.uint8, "w", (2, 3)),
             _req(scales, torch.bfloat16, "scales", (2, 3)), _req(d, torch.bfloat16, "d", 2))
     zp = None if zeros is None else _req(zeros, torch.uint8, "zeros", (2, 3))
@@ -477,7 +498,7 @@ def dg_m_grouped_w4_gemv_nt_ragged(x, w, scales, d, m_offsets, zeros=None, strea
     """The 4-bit product grouped by expert over ragged rows: x [M_total,K], w
     uint8 [G,N,K/2], scales bfloat16 [G,K/group_size,N], zeros uint8 of the
     scales' shape or None, d [M_total,N]; m_offsets int32 [G+1] (device)."""
-    import torch
+    torch = _th()
     ptrs = (_req(x, torch.bfloat16, "x", 2), _req(w, torch.uint8, "w", 3),
             _req(scales, torch.bfloat16, "scales", 3), _req(d, torch.bfloat16, "d", 2),
             _req(m_offsets, torch.int32, "m_offsets", 1))

@@ -20,28 +20,35 @@ dg_status_t check_w4(const void *x, const void *w, const void *s, const void *z,
     if (M < 0 || N <= 0 || K <= 0 || G <= 0) return DG_ERR_INVALID_VALUE;
     if (group_size != 32 && group_size != 64 && group_size != 128) return DG_ERR_UNSUPPORTED_SHAPE;
     if (K % group_size != 0 || N % 8 != 0 || G > 1024) return DG_ERR_UNSUPPORTED_SHAPE;
-    if (K > (1 << 30) || (N + dg::kW4Rows - 1) / dg::kW4Rows > 65535) return DG_ERR_UNSUPPORTED_SHAPE;   // grid.y
+    if (M > 65535 * 32 || K > (1 << 30) || (N + dg::kW4Rows - 1) / dg::kW4Rows > 65535) return DG_ERR_UNSUPPORTED_SHAPE;   // grid.y
     if (!aligned16(x) || !aligned16(w) || !aligned16(s) || !aligned16(z) || !aligned16(d)) return DG_ERR_MISALIGNED;
     return DG_SUCCESS;
 }
 
-template <int kGs, int kNT>
-dg_status_t launch_w4(const dg::W4Params &p, int split, cudaStream_t stream) {
-    using L = dg::W4Smem<kGs, kNT>;
-    auto kernel = dg::w4_gemv_kernel<kGs, kNT>;
+template <int kGs, int kNT, bool kZeros>
+dg_status_t launch_w4(dg::W4Params p, int split, int runs, cudaStream_t stream) {
+    using L = dg::W4Smem<kGs>;
+    auto kernel = dg::w4_gemv_kernel<kGs, kNT, kZeros>;
+    const int blocks = (p.K + dg::kW4BlockK - 1) / dg::kW4BlockK;
+    const int per_cta = (blocks + split - 1) / split;
+    p.tok_cap = p.M < 8 * kNT ? p.M : 8 * kNT;
+    p.chunk = per_cta;
+    if (p.chunk > dg::w4_max_chunk<kNT>()) p.chunk = dg::w4_max_chunk<kNT>();
+    const int smem = L::bytes(p.tok_cap, p.chunk, kZeros);
     // one-time per-device set-up (idempotent; the atomic flag keeps racing first calls defined)
     static std::atomic<bool> configured[kMaxDevices] = {};
     int dev = 0;
     cudaGetDevice(&dev);
     if (!configured[dev].load(std::memory_order_acquire)) {
-        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
+        const int most = L::bytes(8 * kNT, dg::w4_max_chunk<kNT>(), kZeros);
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
         if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(w4 smem)");
         configured[dev].store(true, std::memory_order_release);
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(split, (p.N + dg::kW4Rows - 1) / dg::kW4Rows, p.offsets ? p.G : 1);
+    cfg.gridDim = dim3(split, (p.N + dg::kW4Rows - 1) / dg::kW4Rows, runs);
     cfg.blockDim = dim3(dg::kW4Threads, 1, 1);
-    cfg.dynamicSmemBytes = L::kAlloc;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -51,17 +58,24 @@ dg_status_t launch_w4(const dg::W4Params &p, int split, cudaStream_t stream) {
     cfg.attrs = attr;
     cfg.numAttrs = split > 1 ? 1 : 0;
     if (verbose())
-        std::fprintf(stderr, "[dg] w4_gemv group=%d tokens=%d split=%d grid=%ux%ux%u smem=%d\n", kGs, 8 * kNT, split,
-                     cfg.gridDim.x, cfg.gridDim.y, cfg.gridDim.z, L::kAlloc);
+        std::fprintf(stderr, "[dg] w4_gemv group=%d tokens=%d split=%d grid=%ux%ux%u chunk=%d smem=%d\n", kGs, 8 * kNT,
+                     split, cfg.gridDim.x, cfg.gridDim.y, cfg.gridDim.z, p.chunk, smem);
     cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
     return e == cudaSuccess ? DG_SUCCESS : cuda_fail(e, "w4_gemv_kernel launch");
 }
 
+// experts: those that can have rows (0: dense, a run of rows for each CTA)
+template <int kGs, bool kZeros>
+dg_status_t dispatch_tokens(const dg::W4Params &p, int tokens, int experts, int split, cudaStream_t stream) {
+    if (tokens <= 8) return launch_w4<kGs, 1, kZeros>(p, split, experts ? experts : (p.M + 7) / 8, stream);
+    if (tokens <= 16) return launch_w4<kGs, 2, kZeros>(p, split, experts ? experts : (p.M + 15) / 16, stream);
+    return launch_w4<kGs, 4, kZeros>(p, split, experts ? experts : (p.M + 31) / 32, stream);
+}
+
 template <int kGs>
-dg_status_t dispatch(const dg::W4Params &p, int tokens, int split, cudaStream_t stream) {
-    if (tokens <= 8) return launch_w4<kGs, 1>(p, split, stream);
-    if (tokens <= 16) return launch_w4<kGs, 2>(p, split, stream);
-    return launch_w4<kGs, 4>(p, split, stream);
+dg_status_t dispatch(const dg::W4Params &p, int tokens, int experts, int split, cudaStream_t stream) {
+    if (p.z) return dispatch_tokens<kGs, true>(p, tokens, experts, split, stream);
+    return dispatch_tokens<kGs, false>(p, tokens, experts, split, stream);
 }
 
 dg_status_t w4_gemv(const void *x, const void *w, const void *s, const void *z, void *d, const int32_t *offsets, int M,
@@ -84,16 +98,21 @@ dg_status_t w4_gemv(const void *x, const void *w, const void *s, const void *z, 
     p.K = K;
     p.G = G;
     // tokens a CTA takes at once: all (dense), or what an expert has on average and as much again
-    const int used = offsets ? (M < G ? M : G) : 1;
-    const int tokens = M <= 8 ? M : offsets ? 2 * ((M + used - 1) / used) : M;
-    // K split: the least that gives every SM two CTAs
-    const long long blocks = static_cast<long long>((N + dg::kW4Rows - 1) / dg::kW4Rows) * used;
-    const int stages = (K + dg::kW4StageK - 1) / dg::kW4StageK;
+    const int experts = offsets ? (M < G ? M : G) : 0;
+    const int tokens = M <= 8 || !experts ? M : 2 * ((M + experts - 1) / experts);
+    // K split: until there are two and a half CTAs for each SM, with 4 K blocks or more
+    // in each (fewer cost more in start-up than they save: 16 blocks over 56 row blocks
+    // 7.0 us split by 4, 7.4 by 8), and until no CTA has more than 55, so that the last
+    // ones to finish are short (56 blocks over 512 row blocks: 81 us whole, 70 halved).
+    const long long blocks = static_cast<long long>((N + dg::kW4Rows - 1) / dg::kW4Rows) * (experts ? experts : 1);
+    const int kblocks = (K + dg::kW4BlockK - 1) / dg::kW4BlockK;
     int split = 1;
-    while (split < 8 && blocks * split < 2 * info->num_sms && 2 * split <= stages) split *= 2;
-    if (group_size == 32) return dispatch<32>(p, tokens, split, stream);
-    if (group_size == 64) return dispatch<64>(p, tokens, split, stream);
-    return dispatch<128>(p, tokens, split, stream);
+    while (split < 8 && kblocks / (2 * split) >= 4 &&
+           (blocks * split * 2 < 5LL * info->num_sms || kblocks / split > 55))
+        split *= 2;
+    if (group_size == 32) return dispatch<32>(p, tokens, experts, split, stream);
+    if (group_size == 64) return dispatch<64>(p, tokens, experts, split, stream);
+    return dispatch<128>(p, tokens, experts, split, stream);
 }
 
 }  // namespace

@@ -7,23 +7,31 @@
 // or with expert g's weights for the rows offsets[g] .. offsets[g+1).
 //
 // The weights' bytes are the floor (half a byte and 2/kGs of scale per weight,
-// read once), so the kernel is laid out around streaming them:
-//   * a CTA owns 128 weight rows and a range of K, each of its 8 warps 16 rows;
-//     stages of 256 k (128 bytes of every row, with their x, scales and zero
-//     points) arrive by 16-byte asynchronous copies, kStages in flight;
-//   * a cluster of `split` CTAs shares the 128 rows along K where there are too
-//     few row blocks to fill the GPU; the FP32 partial sums are added in rank
-//     order through distributed shared memory.
+// read once); what stands in the way is the number of instructions that unpack
+// them: at the memory's rate an SM has 2.8 lane instructions for each weight.
+//   * A CTA owns 128 weight rows and a range of K, each of its 4 warps 32 rows.
+//     A warp copies its own rows asynchronously, kDepth blocks of 128 k ahead, and
+//     waits for nobody; x, permuted once to the order in which the products want
+//     it, and the scales are staged by the whole CTA.
+//   * A cluster of `split` CTAs shares the 128 rows along K where there are too
+//     few row blocks to fill the GPU; each CTA stores its FP32 partial sums into
+//     the shared memory of the rows' owners, which add them in rank order.
 // Arithmetic.  A code pair becomes two BF16 numbers by one logic operation
 // (0x4300 | q is 128 + q) and one subtraction of 128 + z, both exact: q - z is
 // an integer of at most 8 bits.  mma.m16n8k16 multiplies 16 weight rows with 8
 // rows of x into an FP32 partial sum of the group, which is then scaled in
-// FP32: no weight is ever rounded.  (At one to a few tokens the products cost
-// a small part of the tensor cores, whichever instruction issues them; what
-// counts is that the sums leave the CUDA cores free to unpack codes.)
-// A lane's word holds 8 consecutive codes; (w >> 4 i) & 0x000F000F takes codes
-// i and i + 4, so x is paired (i, i + 4) too -- the order inside a product is
-// free as long as both operands share it.
+// FP32: no weight is ever rounded.
+//
+// Order of K inside a block of 128.  Both operands of a product may share any
+// order, as long as a product stays inside one scale group.  Word i (8 codes) of
+// lane t of a quad holds the codes from
+//   kGs 128: 32 t + 8 i     kGs 64: 64 (i / 2) + 16 t + 8 (i % 2)     kGs 32: 32 i + 8 t
+// -- one 16-byte, two 8-byte or four 4-byte reads a row -- and x lies in shared
+// memory at [i][t].  (w >> 4 j) & 0x000F000F takes codes j and j + 4 of a word, so
+// each 8 values of x are in pair order (0,4) (1,5) (2,6) (3,7).
+// Rows in shared memory: row 4 g + i of a warp at 64 (8 i + g), its 16-byte
+// pieces permuted by g, so that the copies and all three reads are free of bank
+// conflicts.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -34,10 +42,12 @@
 
 namespace dg {
 
-constexpr int kW4Threads = 256;
+constexpr int kW4Threads = 128;
 constexpr int kW4Rows = 128;            // weight rows per CTA
-constexpr int kW4StageK = 256;          // k per stage: 128 bytes of each row
-constexpr int kW4XPitch = kW4StageK * 2 + 64;   // bytes; 8 rows' 16-byte reads hit distinct banks
+constexpr int kW4BlockK = 128;          // k per block: 16 bytes of a row for each lane of a quad
+constexpr int kW4Depth = 2;             // blocks in flight per warp, a power of two
+constexpr int kW4WarpBlock = 32 * (kW4BlockK / 2);                  // bytes of a warp's rows in a block
+constexpr int kW4RedPitch = kW4Rows;
 constexpr unsigned kW4SiteBadOffsets = 14;
 
 struct W4Params {
@@ -49,25 +59,31 @@ struct W4Params {
     const int32_t *offsets;     // [G + 1]; null: dense
     unsigned *status;
     int M, N, K, G;
+    int tok_cap;                // tokens that shared memory holds: min(8 kNT, M)
+    int chunk;                  // K blocks that it holds
 };
 
-template <int kGs, int kNT>
+// K blocks of x and scales staged at once, at most; a multiple of kW4Depth, small
+// enough for four CTAs on an SM
+template <int kNT>
+constexpr int w4_max_chunk() { return kNT == 1 ? 8 : 4; }
+
+__host__ __device__ constexpr int w4_x_pitch(int chunk) { return chunk * kW4BlockK * 2 + 64; }   // bytes
+
+// Byte offsets: the warps' weight blocks, x (one row more than tokens: zeros), scales, zero points, partial sums.
+template <int kGs>
 struct W4Smem {
-    static constexpr int kGroups = kW4StageK / kGs;
-    static constexpr int kWBytes = kW4Rows * (kW4StageK / 2);
-    static constexpr int kXBytes = 8 * kNT * kW4XPitch;
-    static constexpr int kSBytes = kGroups * kW4Rows * 2;
-    static constexpr int kZBytes = kGroups * kW4Rows;
-    static constexpr int kXOffset = kWBytes;
-    static constexpr int kSOffset = kXOffset + kXBytes;
-    static constexpr int kZOffset = kSOffset + kSBytes;
-    static constexpr int kStageBytes = kZOffset + kZBytes;
-    static constexpr int kStages = kNT == 4 ? 3 : 4;
-    static constexpr int kAlloc = kStages * kStageBytes;
-    // partial sums, [8 kNT][kRedPitch] floats, over the stages
-    static constexpr int kRedPitch = kW4Rows + 4;
-    static_assert(8 * kNT * kRedPitch * 4 <= kAlloc, "partial sums live in the stages");
-    static_assert(kStageBytes % 16 == 0, "16-byte copies");
+    static constexpr int kSBlock = kW4BlockK / kGs * kW4Rows * 2;   // scales of a block
+    static constexpr int kZBlock = kW4BlockK / kGs * kW4Rows;
+    static constexpr int kXOffset = kW4Threads / 32 * kW4Depth * kW4WarpBlock;
+    __host__ __device__ static int s_offset(int tok_cap, int chunk) { return kXOffset + (tok_cap + 1) * w4_x_pitch(chunk); }
+    __host__ __device__ static int z_offset(int tok_cap, int chunk) { return s_offset(tok_cap, chunk) + chunk * kSBlock; }
+    __host__ __device__ static int red_offset(int tok_cap, int chunk, bool zeros) {
+        return z_offset(tok_cap, chunk) + (zeros ? chunk * kZBlock : 0);
+    }
+    static int bytes(int tok_cap, int chunk, bool zeros) {
+        return red_offset(tok_cap, chunk, zeros) + tok_cap * kW4RedPitch * 4;
+    }
 };
 
 namespace w4 {
@@ -75,6 +91,9 @@ namespace w4 {
 // 16 (8) bytes global -> shared; `bytes` of them read, the rest zero
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, uint32_t bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp8(uint32_t dst, const void *src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
@@ -84,35 +103,35 @@ template <int n>
 __device__ __forceinline__ void cp_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory");
 }
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-    uint32_t v;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
-    return v;
-}
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
     return v;
 }
-__device__ __forceinline__ uint32_t lds16(uint32_t a) {
-    uint16_t v;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
     return v;
 }
-__device__ __forceinline__ uint32_t lds8(uint32_t a) {
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
     uint32_t v;
-    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
     return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 __device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
     uint32_t d;
     asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
 }
-// codes i and i + 4 of a word as 128 + q, then minus 128 + z
+// codes i and i + 4 of a word as 128 + q (`bias` 0x43004300), then minus 128 + z
 template <int i>
-__device__ __forceinline__ uint32_t codes(uint32_t w, uint32_t zero) {
-    return sub_bf16x2(((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u, zero);
+__device__ __forceinline__ uint32_t codes(uint32_t w, uint32_t bias, uint32_t zero) {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, 0x000F000F, %2, 0xEA;" : "=r"(d) : "r"(w >> (4 * i)), "r"(bias));   // (a & b) | c
+    return sub_bf16x2(d, zero);
 }
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
@@ -121,29 +140,74 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t a) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(a)
-                 : "memory");
-    return v;
+// the first product of a sum
+__device__ __forceinline__ void mma_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
-// 16-byte chunk `c` of weight row `r` (128 bytes) in a stage: chunks are
-// permuted by the row so that 8 rows' chunks at the same k hit distinct banks
-__device__ __forceinline__ uint32_t w_at(int r, int c) {
-    return static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4));
+
+// 16-byte piece `c` of row 4 g + i of a warp's block
+__device__ __forceinline__ uint32_t w_at(int i, int g, int c) {
+    return static_cast<uint32_t>((8 * i + g) * 64 + ((c ^ ((g & 2) | (g >> 2))) << 4));
+}
+// Place [i][t] of the 8 values from k = 8 c of a block, as i * 4 + t.
+template <int kGs>
+__device__ __forceinline__ int x_slot(int c) {
+    if (kGs == 128) return (c & 3) * 4 + (c >> 2);
+    if (kGs == 64) return ((c >> 3) * 2 + (c & 1)) * 4 + ((c >> 1) & 3);
+    return c;
+}
+
+// The z-th expert that has rows, its first row and the end of them; false if
+// there are fewer.  Offsets are used clamped to [0, M] and raised to the largest
+// before; `record` marks those that were not so.
+__device__ __forceinline__ bool find_expert(const W4Params &p, int z, bool record, int lane, int &expert, int &first,
+                                            int &end) {
+    int run = 0, seen = 0;
+    bool found = false;
+    for (int base = 0; base <= p.G; base += 32) {      // offset i closes expert i - 1
+        const int i = base + lane;
+        const int raw = i <= p.G ? __ldg(p.offsets + i) : 0;
+        int v = min(max(raw, 0), p.M);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v = max(v, u);
+        }
+        v = max(v, run);
+        if (record && i <= p.G && v != raw) atomicCAS(p.status, 0u, 1u | (kW4SiteBadOffsets << 8));
+        int before = __shfl_up_sync(0xffffffffu, v, 1);
+        if (lane == 0) before = run;
+        const bool has = i >= 1 && i <= p.G && v > before;
+        const unsigned mask = __ballot_sync(0xffffffffu, has);
+        if (!found && z < seen + __popc(mask)) {
+            const int src = __fns(mask, 0, z - seen + 1);
+            expert = base + src - 1;
+            first = __shfl_sync(0xffffffffu, before, src);
+            end = __shfl_sync(0xffffffffu, v, src);
+            found = true;
+            if (!record) return true;
+        }
+        seen += __popc(mask);
+        run = __shfl_sync(0xffffffffu, v, 31);
+    }
+    return found;
 }
 
 }  // namespace w4
 
-// grid (split, row blocks, experts), cluster (split, 1, 1)
-template <int kGs, int kNT>
-__global__ void __launch_bounds__(kW4Threads)
+// grid (split, row blocks, experts with rows or runs of 8 kNT tokens), cluster (split, 1, 1)
+template <int kGs, int kNT, bool kZeros>
+__global__ void __launch_bounds__(kW4Threads, kNT == 4 ? 3 : 4)
 w4_gemv_kernel(const W4Params p) {
-    using L = W4Smem<kGs, kNT>;
+    using L = W4Smem<kGs>;
     constexpr int kTok = 8 * kNT;
-    extern __shared__ __align__(128) uint8_t smem[];
+    constexpr int kGroups = kW4BlockK / kGs;        // scale groups of a block
+    constexpr int kWords = 4 / kGroups;             // words of a lane in a group
+    extern __shared__ __align__(128) uint8_t smem[];   // the reads' permutation wants 64
     const uint32_t s_base = ptx::smem_u32(smem);
     const int tid = threadIdx.x;
     const int warp = tid / 32, lane = tid % 32;
@@ -151,160 +215,241 @@ w4_gemv_kernel(const W4Params p) {
     const int split = static_cast<int>(gridDim.x), rank = static_cast<int>(blockIdx.x);
     const int n0 = static_cast<int>(blockIdx.y) * kW4Rows;
 
-    int first = 0, end = p.M;
-    const size_t e = blockIdx.z;
+    int expert = 0, first = static_cast<int>(blockIdx.z) * kTok, end = min(p.M, first + kTok);
     if (p.offsets) {
-        // this expert's rows: clamped to the buffer, never before an earlier offset
-        const int g = static_cast<int>(e);
-        int lo = 0;
-        for (int i = lane; i <= g; i += 32) {
-            const int raw = __ldg(p.offsets + i);
-            lo = max(lo, min(max(raw, 0), p.M));
-        }
-        lo = __reduce_max_sync(0xffffffffu, lo);
-        const int raw_lo = __ldg(p.offsets + g), raw_hi = __ldg(p.offsets + g + 1);
-        first = lo;
-        end = max(lo, min(max(raw_hi, 0), p.M));
-        if ((raw_lo != first || raw_hi != end) && tid == 0) atomicCAS(p.status, 0u, 1u | (kW4SiteBadOffsets << 8));
+        const int z = static_cast<int>(blockIdx.z);
+        const bool record = z == 0 && rank == 0 && n0 == 0 && warp == 0;
+        if (!w4::find_expert(p, z, record, lane, expert, first, end)) return;   // the whole cluster: it shares z
     }
-    if (first >= end) return;                       // the whole cluster: its CTAs share the expert
 
-    const int num_st = (p.K + kW4StageK - 1) / kW4StageK;
-    const int st0 = num_st * rank / split, st1 = num_st * (rank + 1) / split;
+    const int num_blk = (p.K + kW4BlockK - 1) / kW4BlockK;
+    const int blk0 = static_cast<int>(static_cast<long long>(num_blk) * rank / split);
+    const int blk1 = static_cast<int>(static_cast<long long>(num_blk) * (rank + 1) / split);
+    const size_t e = static_cast<size_t>(expert);
     const size_t groups = static_cast<size_t>(p.K / kGs);
-    const uint8_t *w = p.w + (e * p.N) * static_cast<size_t>(p.K / 2);
     const __nv_bfloat16 *sc = p.s + e * groups * p.N + n0;
-    const uint8_t *zp = p.z ? p.z + e * groups * p.N + n0 : nullptr;
+    const uint8_t *zp = kZeros ? p.z + e * groups * p.N + n0 : nullptr;
     const int rows_left = p.N - n0;
+    const int r0 = warp * 32 + 4 * g8;              // this lane's rows r0 .. r0 + 3 of the CTA's (rows past N: row N - 1)
+    const uint8_t *wrow[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        wrow[i] = p.w + (e * p.N + n0 + min(r0 + i, rows_left - 1)) * static_cast<size_t>(p.K / 2) + t4 * 16;
+    const uint32_t x_pitch = w4_x_pitch(p.chunk);
+    const uint32_t s_off = s_base + L::s_offset(p.tok_cap, p.chunk) + r0 * 2;
+    const uint32_t z_off = s_base + L::z_offset(p.tok_cap, p.chunk) + r0;
+
+    // first of this lane's reads of a row: a 16-byte piece, 8 bytes or a word of one
+    const uint32_t w_read = s_base + warp * (kW4Depth * kW4WarpBlock) +
+                            (kGs == 128 ? w4::w_at(0, g8, t4)
+                             : kGs == 64 ? w4::w_at(0, g8, t4 >> 1) + (t4 & 1) * 8 : w4::w_at(0, g8, 0) + t4 * 4);
+    const uint32_t w_off = s_base + warp * (kW4Depth * kW4WarpBlock);
+    const uint32_t red_off = s_base + L::red_offset(p.tok_cap, p.chunk, kZeros);
+    const uint32_t zero_row = s_base + L::kXOffset + p.tok_cap * x_pitch;
+    uint32_t bias;
+    asm volatile("mov.u32 %0, 0x43004300;" : "=r"(bias));
+    for (int i = tid * 16; i < static_cast<int>(x_pitch); i += kW4Threads * 16)
+        w4::sts128(zero_row + i, make_uint4(0u, 0u, 0u, 0u));
+    if (split > 1) ptx::cluster_arrive_relaxed();   // waited for before the first store into another CTA
+    bool started = split == 1;
+
+    // A warp's rows of block `blk`, whose slot `u` is blk - blk0 modulo kW4Depth, from
+    // `ahead` bytes past wptr; zeros past K.
+    const uint8_t *wptr[4];
+    const int full = min(blk1, p.K / kW4BlockK);
+    const uint32_t w_copy = w_off + w4::w_at(0, g8, t4);
+    auto copy = [&](int blk, int u, int ahead) {
+        if (blk < full) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w4::cp16(w_copy + u * kW4WarpBlock + i * 512, wptr[i] + ahead);
+        } else if (blk < blk1) {                   // the last block, where K ends inside it
+            const uint32_t bytes = blk * kW4BlockK + t4 * 32 < p.K ? 16u : 0u;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                w4::cp16(w_copy + u * kW4WarpBlock + i * 512, bytes ? wptr[i] + ahead : p.w, bytes);
+        }
+        w4::cp_commit();
+    };
 
     for (int m0 = first; m0 < end; m0 += kTok) {
         const int ntok = min(kTok, end - m0);
-        auto issue = [&](int st) {
-            const uint32_t base = s_base + (st - st0) % L::kStages * L::kStageBytes;
-            const int k0 = st * kW4StageK;
-            const int kv = min(kW4StageK, p.K - k0);
+        float acc[2][kNT][4];
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int i = 0; i < kNT; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[r][i][j] = 0.f;
+        // where this lane's rows of x lie: tokens past the expert's read zeros
+        uint32_t xrow[kNT];
+#pragma unroll
+        for (int n = 0; n < kNT; ++n)
+            xrow[n] = (8 * n + g8 < ntok ? s_base + L::kXOffset + (8 * n + g8) * x_pitch : zero_row) + t4 * 16;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) wptr[i] = wrow[i] + static_cast<size_t>(blk0) * (kW4BlockK / 2);
+#pragma unroll
+        for (int d = 0; d < kW4Depth; ++d) copy(blk0 + d, d, d * (kW4BlockK / 2));
+
+        for (int c0 = blk0; c0 < blk1; c0 += p.chunk) {
+            const int c1 = min(c0 + p.chunk, blk1);
+            if (c0 != blk0) __syncthreads();       // the chunk before has been read
+            // scales and zero points; groups past K: zero
+            for (int i = tid; i < (c1 - c0) * kGroups * 16; i += kW4Threads) {
+                const int j = i >> 4, c = i & 15;
+                if (c * 8 < rows_left) {
+                    const int grp = c0 * kGroups + j;
+                    const bool ok = grp < static_cast<int>(groups);
+                    const size_t at = static_cast<size_t>(ok ? grp : 0) * p.N + c * 8;
+                    w4::cp16(s_base + L::s_offset(p.tok_cap, p.chunk) + j * (kW4Rows * 2) + c * 16, sc + at, ok ? 16u : 0u);
+                    if (kZeros) w4::cp8(s_base + L::z_offset(p.tok_cap, p.chunk) + j * kW4Rows + c * 8, zp + at);
+                }
+            }
+            w4::cp_commit();
+            // x, 8 values at a time, in the products' order; zeros past K.  Thread: piece
+            // tid % 16 of each block, tokens tid / 16, tid / 16 + 8, ...
             {
-                const int c = tid & 7, r0 = tid >> 3;
-                if (c * 32 < kv) {
+                const int c = tid & 15;
+                const int have = (p.K - c0 * kW4BlockK - c * 8 + kW4BlockK - 1) / kW4BlockK;   // blocks whose piece lies below K
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int r = r0 + 32 * i;
-                        const int n = min(r, rows_left - 1);        // rows past N: any row, not stored
-                        w4::cp16(base + w4::w_at(r, c),
-                                 w + (static_cast<size_t>(n0 + n) * p.K + k0) / 2 + c * 16, 16u);
+                for (int n = 0; n < kNT; ++n) {
+                    const int tok = 8 * n + (tid >> 4);
+                    if (tok < ntok) {
+                        const uint4 *src = reinterpret_cast<const uint4 *>(
+                            p.x + static_cast<size_t>(m0 + tok) * p.K + static_cast<size_t>(c0) * kW4BlockK) + c;
+                        uint32_t dst = s_base + L::kXOffset + tok * x_pitch + w4::x_slot<kGs>(c) * 16;
+#pragma unroll 4
+                        for (int b = 0; b < c1 - c0; ++b) {
+                            const uint4 v = b < have ? __ldg(src + b * 16) : make_uint4(0u, 0u, 0u, 0u);
+                            w4::sts128(dst + b * 256,
+                                       make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
+                                                  __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632)));
+                        }
                     }
                 }
             }
+            w4::cp_wait<0>();
+            __syncthreads();
+            uint32_t xa[kNT], sa = s_off, za = z_off;
 #pragma unroll
-            for (int i = 0; i < kNT; ++i) {
-                const int tok = (tid >> 5) + 8 * i, c = tid & 31;
-                if (c * 8 < kv) {
-                    const bool ok = tok < ntok;                     // tokens past the expert's: zeros
-                    w4::cp16(base + L::kXOffset + tok * kW4XPitch + c * 16,
-                             p.x + static_cast<size_t>(m0 + (ok ? tok : 0)) * p.K + k0 + c * 8, ok ? 16u : 0u);
-                }
-            }
-            const int c = tid & 15, j = tid >> 4;
-            if (j < kv / kGs && c * 8 < rows_left) {
-                const size_t at = static_cast<size_t>(k0 / kGs + j) * p.N + c * 8;
-                w4::cp16(base + L::kSOffset + j * (kW4Rows * 2) + c * 16, sc + at, 16u);
-                if (zp) w4::cp8(base + L::kZOffset + j * kW4Rows + c * 8, zp + at);
-            }
-        };
-
-        float acc[kNT][4];
+            for (int n = 0; n < kNT; ++n) xa[n] = xrow[n];
+            // a chunk starts at a multiple of kW4Depth blocks from blk0: block b0 + u lies in slot u
+            for (int b0 = c0; b0 < c1; b0 += kW4Depth) {
 #pragma unroll
-        for (int i = 0; i < kNT; ++i)
+                for (int u = 0; u < kW4Depth; ++u) {
+                    if (b0 + u >= c1) break;
+                    w4::cp_wait<kW4Depth - 1>();
+                    __syncwarp();                  // every lane's copies of this block have landed
 #pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
-
+                    for (int j = 0; j < kGroups; ++j) {
+                        uint32_t zero[4] = {0x43084308u, 0x43084308u, 0x43084308u, 0x43084308u};
+                        if constexpr (kZeros) {
+                            const uint32_t zb = w4::lds32(za + u * L::kZBlock + j * kW4Rows) & 0x7F7F7F7Fu;
 #pragma unroll
-        for (int i = 0; i < L::kStages - 1; ++i) {
-            if (st0 + i < st1) issue(st0 + i);
-            w4::cp_commit();
-        }
-        const int r = warp * 16 + g8;
-        for (int st = st0; st < st1; ++st) {
-            w4::cp_wait<L::kStages - 2>();
-            __syncthreads();                       // stage st has landed; stage st - 1 is free
-            if (st + L::kStages - 1 < st1) issue(st + L::kStages - 1);
-            w4::cp_commit();
-            const uint32_t base = s_base + (st - st0) % L::kStages * L::kStageBytes;
-            const int kv = min(kW4StageK, p.K - st * kW4StageK);
+                            for (int i = 0; i < 4; ++i) zero[i] = __byte_perm(zb, 0x43u, 0x4040 + i * 0x0101);   // 128 + z
+                        }
+                        uint32_t w[4][kWords];
+                        const uint32_t wa = (w_read ^ (j * (64 / kGroups))) + u * kW4WarpBlock;
 #pragma unroll
-            for (int j = 0; j < L::kGroups; ++j) {
-                if (j * kGs >= kv) break;
-                uint32_t z_lo = 0x43084308u, z_hi = 0x43084308u;
-                if (zp) {
-                    z_lo = (0x4300u | (w4::lds8(base + L::kZOffset + j * kW4Rows + r) & 0x7Fu)) * 0x10001u;
-                    z_hi = (0x4300u | (w4::lds8(base + L::kZOffset + j * kW4Rows + r + 8) & 0x7Fu)) * 0x10001u;
-                }
-                float c[kNT][4];
+                        for (int i = 0; i < 4; ++i) {
+                            if constexpr (kGs == 128) {
+                                const uint4 v = w4::lds128(wa + i * 512);
+                                w[i][0] = v.x; w[i][1] = v.y; w[i][2] = v.z; w[i][3] = v.w;
+                            } else if constexpr (kGs == 64) {
+                                const uint2 v = w4::lds64(wa + i * 512);
+                                w[i][0] = v.x; w[i][1] = v.y;
+                            } else {
+                                w[i][0] = w4::lds32(wa + i * 512);
+                            }
+                        }
+                        float c[2][kNT][4];
 #pragma unroll
-                for (int i = 0; i < kNT; ++i)
+                        for (int k = 0; k < kWords; ++k) {
+                            uint4 x[kNT];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) c[i][q] = 0.f;
+                            for (int n = 0; n < kNT; ++n) x[n] = w4::lds128(xa[n] + u * 256 + (j * kWords + k) * 64);
 #pragma unroll
-                for (int b = j * kGs / 32; b < (j + 1) * kGs / 32; ++b) {
-                    const uint32_t lo = w4::lds32(base + w4::w_at(r, b) + t4 * 4);
-                    const uint32_t hi = w4::lds32(base + w4::w_at(r + 8, b) + t4 * 4);
-                    const uint32_t l0 = w4::codes<0>(lo, z_lo), l1 = w4::codes<1>(lo, z_lo),
-                                   l2 = w4::codes<2>(lo, z_lo), l3 = w4::codes<3>(lo, z_lo);
-                    const uint32_t h0 = w4::codes<0>(hi, z_hi), h1 = w4::codes<1>(hi, z_hi),
-                                   h2 = w4::codes<2>(hi, z_hi), h3 = w4::codes<3>(hi, z_hi);
+                            for (int r = 0; r < 2; ++r) {
+                                const uint32_t lo = w[2 * r][k], hi = w[2 * r + 1][k];
+                                const uint32_t zl = zero[2 * r], zh = zero[2 * r + 1];
+                                const uint32_t l0 = w4::codes<0>(lo, bias, zl), l1 = w4::codes<1>(lo, bias, zl),
+                                               l2 = w4::codes<2>(lo, bias, zl), l3 = w4::codes<3>(lo, bias, zl);
+                                const uint32_t h0 = w4::codes<0>(hi, bias, zh), h1 = w4::codes<1>(hi, bias, zh),
+                                               h2 = w4::codes<2>(hi, bias, zh), h3 = w4::codes<3>(hi, bias, zh);
 #pragma unroll
-                    for (int i = 0; i < kNT; ++i) {
-                        const uint4 x = w4::lds128(base + L::kXOffset + (8 * i + g8) * kW4XPitch + b * 64 + t4 * 16);
-                        w4::mma(c[i], l0, h0, l1, h1, __byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632));
-                        w4::mma(c[i], l2, h2, l3, h3, __byte_perm(x.y, x.w, 0x5410), __byte_perm(x.y, x.w, 0x7632));
+                                for (int n = 0; n < kNT; ++n) {
+                                    if (k == 0) w4::mma_first(c[r][n], l0, h0, l1, h1, x[n].x, x[n].y);
+                                    else w4::mma(c[r][n], l0, h0, l1, h1, x[n].x, x[n].y);
+                                    w4::mma(c[r][n], l2, h2, l3, h3, x[n].z, x[n].w);
+                                }
+                            }
+                        }
+                        const uint2 sv = w4::lds64(sa + u * L::kSBlock + j * (kW4Rows * 2));
+                        const float s4[4] = {__uint_as_float(sv.x << 16), __uint_as_float(sv.x & 0xFFFF0000u),
+                                             __uint_as_float(sv.y << 16), __uint_as_float(sv.y & 0xFFFF0000u)};
+#pragma unroll
+                        for (int r = 0; r < 2; ++r)
+#pragma unroll
+                            for (int n = 0; n < kNT; ++n) {
+                                acc[r][n][0] = fmaf(s4[2 * r], c[r][n][0], acc[r][n][0]);
+                                acc[r][n][1] = fmaf(s4[2 * r], c[r][n][1], acc[r][n][1]);
+                                acc[r][n][2] = fmaf(s4[2 * r + 1], c[r][n][2], acc[r][n][2]);
+                                acc[r][n][3] = fmaf(s4[2 * r + 1], c[r][n][3], acc[r][n][3]);
+                            }
                     }
+                    __syncwarp();                  // every lane has read this block
+                    copy(b0 + u + kW4Depth, u, (u + kW4Depth) * (kW4BlockK / 2));
                 }
-                const float s_lo = __uint_as_float(w4::lds16(base + L::kSOffset + (j * kW4Rows + r) * 2) << 16);
-                const float s_hi = __uint_as_float(w4::lds16(base + L::kSOffset + (j * kW4Rows + r + 8) * 2) << 16);
 #pragma unroll
-                for (int i = 0; i < kNT; ++i) {
-                    acc[i][0] = fmaf(s_lo, c[i][0], acc[i][0]);
-                    acc[i][1] = fmaf(s_lo, c[i][1], acc[i][1]);
-                    acc[i][2] = fmaf(s_hi, c[i][2], acc[i][2]);
-                    acc[i][3] = fmaf(s_hi, c[i][3], acc[i][3]);
-                }
+                for (int i = 0; i < 4; ++i) wptr[i] += kW4Depth * (kW4BlockK / 2);
+#pragma unroll
+                for (int n = 0; n < kNT; ++n) xa[n] += kW4Depth * 256;
+                sa += kW4Depth * L::kSBlock;
+                za += kW4Depth * L::kZBlock;
             }
         }
-        // partial sums [token][row] over the stages, then the sum over the cluster
-        w4::cp_wait<0>();
-        __syncthreads();
-        float *red = reinterpret_cast<float *>(smem);
-#pragma unroll
-        for (int i = 0; i < kNT; ++i) {
-            float *at = red + (8 * i + 2 * t4) * L::kRedPitch + r;
-            at[0] = acc[i][0];
-            at[L::kRedPitch] = acc[i][1];
-            at[8] = acc[i][2];
-            at[L::kRedPitch + 8] = acc[i][3];
+        // This lane's sums of 4 rows for 2 kNT tokens go to the rows' owner: rank
+        // r adds rows 128 r / split .. and keeps [source rank][token][its rows].
+        const int own = kW4Rows / split;            // rows per owner, at least 16
+        const uint32_t slot = red_off + static_cast<uint32_t>(rank * p.tok_cap * own + (r0 & (own - 1))) * 4u;
+        const uint32_t dst = split > 1 ? ptx::map_cluster(slot, static_cast<uint32_t>(r0 / own)) : slot;
+        if (!started) {
+            ptx::cluster_wait_acquire();            // every CTA of the cluster has started
+            started = true;
         }
+#pragma unroll
+        for (int n = 0; n < kNT; ++n)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int tok = 8 * n + 2 * t4 + q;
+                if (tok < ntok)
+                    ptx::st_cluster_v4(dst + static_cast<uint32_t>(tok * own) * 4u, acc[0][n][q], acc[0][n][2 + q],
+                                       acc[1][n][q], acc[1][n][2 + q]);
+            }
         if (split > 1) ptx::cluster_sync_all();
         else __syncthreads();
-        const int quads = kW4Rows / 4 / split;      // this CTA's runs of 4 rows
+        const int quads = own / 4;                  // this CTA's runs of 4 rows
+        const float *red = reinterpret_cast<const float *>(smem + (red_off - s_base));
         for (int i = tid; i < quads * ntok; i += kW4Threads) {
-            const int tok = i / quads, q = rank * quads + i % quads;
-            const uint32_t at = s_base + static_cast<uint32_t>(tok * L::kRedPitch + 4 * q) * 4u;
+            const int tok = i / quads, q = i - tok * quads;
             float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
             for (int c = 0; c < split; ++c) {
-                const float4 v = split > 1 ? w4::ld_cluster_f4(ptx::map_cluster(at, static_cast<uint32_t>(c)))
-                                           : *reinterpret_cast<const float4 *>(red + tok * L::kRedPitch + 4 * q);
+                const float4 v = *reinterpret_cast<const float4 *>(red + (c * p.tok_cap + tok) * own + 4 * q);
                 sum.x += v.x; sum.y += v.y; sum.z += v.z; sum.w += v.w;
             }
-            if (4 * q < rows_left) {
+            const int row = rank * own + 4 * q;
+            if (row < rows_left) {
                 const __nv_bfloat162 a = __floats2bfloat162_rn(sum.x, sum.y), b = __floats2bfloat162_rn(sum.z, sum.w);
                 uint2 o;
                 o.x = *reinterpret_cast<const uint32_t *>(&a);
                 o.y = *reinterpret_cast<const uint32_t *>(&b);
-                *reinterpret_cast<uint2 *>(p.d + static_cast<size_t>(m0 + tok) * p.N + n0 + 4 * q) = o;
+                *reinterpret_cast<uint2 *>(p.d + static_cast<size_t>(m0 + tok) * p.N + n0 + row) = o;
             }
         }
-        // the partial sums are read before the stages are written again or the CTA leaves
-        if (split > 1) ptx::cluster_sync_all();
-        else __syncthreads();
+        // with more tokens to come: the sums have been read before anybody stores the next ones
+        if (m0 + kTok < end) {
+            if (split > 1) ptx::cluster_sync_all();
+            else __syncthreads();
+        }
     }
 }
 
