@@ -27,6 +27,12 @@
 //     rows and only then hands the stage to the MMA warp.  The block comes last,
 //     so the MMAs of the blocks before it run meanwhile.
 //
+// Output.  A lane holds one row of the accumulator; stored straight from there,
+// each instruction touches 32 lines (wgrad of 64 experts, 62 tokens each, 1000 x
+// 2112, BF16: 174 us, against 46 for its bytes).  So a warp gathers 32 x 32 boxes in
+// shared memory and TMA stores write them, clipped at N (and at M, kTN).  Boxes that
+// cross an expert's last row (kNT, kNN) and sums added to d are stored by the lanes.
+//
 // Roles: warp 0 producer (TMA), warp 1 TMEM and MMA issue, warp 2 clears ragged
 // token rows (kTN), warps 4..11 epilogue: warp w drains TMEM lanes 32 (w % 4),
 // columns of half (w - 4) / 4.  Persistent; two accumulators in rotation, so
@@ -71,7 +77,7 @@ struct RaggedParams {
     int debug_flags;
 };
 
-template <int kDir, int kBN, int kStages, int kCtaGroup>
+template <int kDir, int kBN, int kStages, int kCtaGroup, bool kF32>
 struct RaggedSmem {
     static constexpr int kABytes = kTileX * 128;
     static constexpr int kBCols = kBN / kCtaGroup;            // this CTA's columns of B
@@ -83,7 +89,11 @@ struct RaggedSmem {
     static constexpr int kMiscOffset = kBarOffset + kNumBars * 8;   // tmem addr, abort flag
     static constexpr int kOffsOffset = (kMiscOffset + 16 + 15) / 16 * 16;
     static constexpr int kPrefixOffset = kOffsOffset + (kMaxGroups + 1) * 4;
-    static constexpr int kUsed = kPrefixOffset + (kMaxGroups + 1) * 4;
+    // epilogue: boxes of 32 rows by 32 columns, 4 KB for each of the 8 warps
+    static constexpr int kBoxBytes = 32 * 32 * (kF32 ? 4 : 2);
+    static constexpr int kBoxes = 4096 / kBoxBytes;
+    static constexpr int kOutOffset = (kPrefixOffset + (kMaxGroups + 1) * 4 + 1023) / 1024 * 1024;
+    static constexpr int kUsed = kOutOffset + 8 * 4096;
     static constexpr int kAlloc = (kUsed + 1024 > kMinSmem) ? kUsed + 1024 : kMinSmem;
     static constexpr int kTmemCols = kAccBufs * kBN <= 128 ? 128 : kAccBufs * kBN <= 256 ? 256 : 512;
     static_assert(kBN == 64 || kBN == 128 || kBN == 256, "tile N");
@@ -197,12 +207,31 @@ __device__ __forceinline__ void store8(void *d, size_t index, const float *v, bo
     }
 }
 
+// 32 columns of this lane's row into a warp's box of 32 rows, in the order of the
+// TMA store's swizzle (64 bytes a row for BF16, 128 for FP32).
+template <bool kF32>
+__device__ __forceinline__ void stage32(uint8_t *box, int lane, const float *v) {
+    if constexpr (kF32) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<float4 *>(box + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+                make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint4 *>(box + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
+                make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
+                           pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
+    }
+}
+
 // tm_a, tm_b: see the operand table above (kNT, kNN single-CTA: A boxes of 32 rows).
+// tm_d: boxes of 32 columns by 32 rows of D [groups][rows][N] (kTN: one group per expert).
 template <int kDir, int kBN, int kStages, int kCtaGroup, bool kF32>
 __global__ void __launch_bounds__(kRaggedThreads, 1)
 ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
-                   const RaggedParams p) {
-    using L = RaggedSmem<kDir, kBN, kStages, kCtaGroup>;
+                   const __grid_constant__ CUtensorMap tm_d, const RaggedParams p) {
+    using L = RaggedSmem<kDir, kBN, kStages, kCtaGroup, kF32>;
     using TM = RaggedMap<kDir, kBN, kCtaGroup>;
     static_assert(!kF32 || kDir == kTN, "FP32 output: weight gradient");
     constexpr bool kPair = kCtaGroup == 2;
@@ -239,6 +268,7 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
     if (threadIdx.x == 0) {
         ptx::prefetch_tmap(&tm_a);
         ptx::prefetch_tmap(&tm_b);
+        ptx::prefetch_tmap(&tm_d);
         for (int i = 0; i < kStages; ++i) {
             // kTN: one arrival per CTA (its producer, or its row-clearing warp)
             ptx::mbar_init(full_bar(i), kDir == kTN ? kCtaGroup : 1);
@@ -478,7 +508,8 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
         const int quarter = warp & 3;
         const int half = (warp - kEpiWarp0) >> 2;
         const int lrow = pair_rank * kTileX + quarter * 32 + lane;
-        int buf = 0;
+        uint8_t *out = smem + L::kOutOffset + (warp - kEpiWarp0) * 4096;
+        int buf = 0, out_buf = 0;
         uint32_t tphase = 0;
         bool ok = true;
         auto release = [&]() {
@@ -500,11 +531,40 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
                                 static_cast<size_t>(p.N);
             const int c0 = tl.n0 + half * kHalf;
             const bool add = kDir == kTN && p.accumulate;
+            // the warp's 32 rows as a box: clipped by the map (kTN) or inside the expert
+            const int box_row = tl.row0 + pair_rank * kTileX + quarter * 32;
+            const bool boxed = !add && (kDir == kTN ? box_row < tl.row_end : box_row + 32 <= tl.row_end);
+            auto put = [&](int c, const float *v) {      // columns c0 + c .. + 31 of this lane's row
+                if (boxed) {
+                    if (c0 + c < p.N) {
+                        if (lane == 0) {           // what this box held before has been read
+                            if (L::kBoxes == 2) ptx::bulk_wait_read1();
+                            else ptx::bulk_wait_read0();
+                        }
+                        __syncwarp();
+                        uint8_t *box = out + (out_buf ? L::kBoxBytes : 0);
+                        stage32<kF32>(box, lane, v);
+                        ptx::fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            ptx::tma_store_3d(&tm_d, ptx::smem_u32(box), c0 + c, box_row, kDir == kTN ? tl.g : 0);
+                            ptx::bulk_commit();
+                        }
+                        out_buf ^= L::kBoxes - 1;
+                    }
+                } else if (row_ok) {
+#pragma unroll
+                    for (int j = 0; j < 32; j += 8)
+                        if (c0 + c + j < p.N) store8<kF32>(p.d, base + c0 + c + j, v + j, add);
+                }
+            };
             if (tl.num_kb == 0) {                  // kTN, an expert without tokens
-                if (!add && row_ok) {
-                    const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                    for (int j = 0; j < kHalf; j += 8)
-                        if (c0 + j < p.N) store8<kF32>(p.d, base + c0 + j, zero, false);
+                if (!add) {
+                    float zero[32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) zero[j] = 0.f;
+#pragma unroll 1
+                    for (int c = 0; c < kHalf; c += 32) put(c, zero);
                 }
                 continue;
             }
@@ -528,11 +588,8 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
                     release();
                 }
                 if (!ok) break;
-                if (row_ok) {
 #pragma unroll
-                    for (int j = 0; j < kHalf; j += 8)
-                        if (c0 + j < p.N) store8<kF32>(p.d, base + c0 + j, acc + j, add);
-                }
+                for (int c = 0; c < kHalf; c += 32) put(c, acc + c);
             } else {
                 if (!wait(tfull_bar(buf), tphase, kSitePromoFull)) { ok = false; break; }
                 ptx::tc_fence_after();
@@ -543,15 +600,13 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
                     float v[32];
                     ptx::tmem_ld32p(taddr + c, v);
                     ptx::tmem_wait_ld();
-                    if (row_ok) {
-#pragma unroll
-                        for (int j = 0; j < 32; j += 8)
-                            if (c0 + c + j < p.N) store8<kF32>(p.d, base + c0 + c + j, v + j, add);
-                    }
+                    put(c, v);
                 }
                 release();
             }
         }
+        if (lane == 0) ptx::bulk_wait0();          // never leave with stores reading shared memory
+        __syncwarp();
     }
 
     // ---------------------------------------------------------------- teardown
