@@ -45,9 +45,4 @@ long long timeout_cycles();
 dg_status_t make_kmajor_map(CUtensorMap *m, const void *base, int elem_bytes, long long K,
                             long long rows, long long groups, int box_rows);
 
-// 3-D tensor map {N, rows, groups} of an output of elem_bytes-wide elements (2:
-// BF16, 4: FP32) for boxes of 32 columns by 32 rows, their rows swizzled over 64
-// (BF16) or 128 bytes; what lies outside is not written.
-dg_status_t make_out_map(CUtensorMap *m, void *base, int elem_bytes, long long N, long long rows, long long groups);
-
 }  // namespace dg_host

@@ -134,30 +134,6 @@ dg_status_t make_kmajor_map(CUtensorMap *m, const void *base, int elem_bytes, lo
     return DG_SUCCESS;
 }
 
-dg_status_t make_out_map(CUtensorMap *m, void *base, int elem_bytes, long long N, long long rows, long long groups) {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) {
-        std::snprintf(t_last_cuda_error, sizeof(t_last_cuda_error),
-                      "cuTensorMapEncodeTiled entry point unavailable");
-        return DG_ERR_CUDA;
-    }
-    const cuuint64_t eb = static_cast<cuuint64_t>(elem_bytes);
-    cuuint64_t dims[3] = {static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(groups)};
-    cuuint64_t strides[2] = {static_cast<cuuint64_t>(N) * eb, static_cast<cuuint64_t>(N) * static_cast<cuuint64_t>(rows) * eb};
-    cuuint32_t box[3] = {32, 32, 1};
-    cuuint32_t estr[3] = {1, 1, 1};
-    CUresult r = fn(m, elem_bytes == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base,
-                    dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                    elem_bytes == 4 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                    CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) {
-        std::snprintf(t_last_cuda_error, sizeof(t_last_cuda_error),
-                      "cuTensorMapEncodeTiled failed (CUresult %d)", static_cast<int>(r));
-        return DG_ERR_CUDA;
-    }
-    return DG_SUCCESS;
-}
-
 long long timeout_cycles() {
     static long long v = [] {
         const char *s = std::getenv("DG_WAIT_TIMEOUT_CYCLES");

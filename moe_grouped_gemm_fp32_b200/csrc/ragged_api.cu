@@ -37,7 +37,7 @@ struct Launch {
     static void config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute *attr, int grid, cudaStream_t stream) {
         cfg = {};
         cfg.gridDim = dim3(grid, 1, 1);
-        cfg.blockDim = dim3(dg::kRaggedThreads, 1, 1);
+        cfg.blockDim = dim3(dg::ragged_threads(kF32), 1, 1);
         cfg.dynamicSmemBytes = L::kAlloc;
         cfg.stream = stream;
         cfg.attrs = attr;
@@ -81,8 +81,8 @@ struct Launch {
     }
 
     // tiles: an upper bound of the tile count
-    static dg_status_t run(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &md,
-                           const dg::RaggedParams &p, long long tiles, const DeviceInfo *info, cudaStream_t stream) {
+    static dg_status_t run(const CUtensorMap &ma, const CUtensorMap &mb, const dg::RaggedParams &p, long long tiles,
+                           const DeviceInfo *info, cudaStream_t stream) {
         int units = 0;
         dg_status_t st = setup(info, &units);
         if (st != DG_SUCCESS) return st;
@@ -93,7 +93,7 @@ struct Launch {
         cudaLaunchConfig_t cfg;
         cudaLaunchAttribute attr[1];
         config(cfg, attr, grid, stream);
-        cudaError_t e = cudaLaunchKernelEx(&cfg, kernel(), ma, mb, md, p);
+        cudaError_t e = cudaLaunchKernelEx(&cfg, kernel(), ma, mb, p);
         return e == cudaSuccess ? DG_SUCCESS : cuda_fail(e, "ragged_gemm_kernel launch");
     }
 };
@@ -132,29 +132,27 @@ dg_status_t m_grouped(const void *a, const void *b, void *d, const int32_t *offs
     // 256-row CTA pairs where an expert has 128 rows or more on average
     const bool pair = N > 128 && T >= 256 && T / used >= 128;
     const int bn = pair ? 256 : ceil_div(N, 128) * used >= info->num_sms ? 128 : 64;
-    CUtensorMap ma, mb, md;
+    CUtensorMap ma, mb;
     if ((st = make_kmajor_map(&ma, a, 2, K, T, 1, pair ? 128 : 32)) != DG_SUCCESS) return st;
     st = kDir == dg::kNT ? make_kmajor_map(&mb, b, 2, K, N, G, pair ? bn / 2 : bn)
                          : make_kmajor_map(&mb, b, 2, N, K, G, dg::kRaggedBlockK);
     if (st != DG_SUCCESS) return st;
-    if ((st = make_out_map(&md, d, 2, N, T, 1)) != DG_SUCCESS) return st;
     const long long tiles = (ceil_div(T, pair ? 256 : 128) + used) * ceil_div(N, bn);
-    if (pair) return Launch<kDir, 256, 5, 2, false>::run(ma, mb, md, p, tiles, info, stream);
-    if (bn == 128) return Launch<kDir, 128, 5, 1, false>::run(ma, mb, md, p, tiles, info, stream);
-    return Launch<kDir, 64, 7, 1, false>::run(ma, mb, md, p, tiles, info, stream);
+    if (pair) return Launch<kDir, 256, 5, 2, false>::run(ma, mb, p, tiles, info, stream);
+    if (bn == 128) return Launch<kDir, 128, 5, 1, false>::run(ma, mb, p, tiles, info, stream);
+    return Launch<kDir, 64, 7, 1, false>::run(ma, mb, p, tiles, info, stream);
 }
 
 template <bool kF32>
 dg_status_t k_grouped(const void *a, const void *b, const dg::RaggedParams &p, const DeviceInfo *info,
                       cudaStream_t stream) {
-    CUtensorMap ma, mb, md;
+    CUtensorMap ma, mb;
     dg_status_t st = make_kmajor_map(&ma, a, 2, p.M, p.T, 1, dg::kRaggedBlockK);
     if (st != DG_SUCCESS) return st;
     if ((st = make_kmajor_map(&mb, b, 2, p.N, p.T, 1, dg::kRaggedBlockK)) != DG_SUCCESS) return st;
-    if ((st = make_out_map(&md, p.d, kF32 ? 4 : 2, p.N, p.M, p.G)) != DG_SUCCESS) return st;
     if (p.M > 128 && p.N > 128)
-        return Launch<dg::kTN, 256, 5, 2, kF32>::run(ma, mb, md, p, p.G * ceil_div(p.M, 256) * ceil_div(p.N, 256), info, stream);
-    return Launch<dg::kTN, 128, 5, 1, kF32>::run(ma, mb, md, p, p.G * ceil_div(p.M, 128) * ceil_div(p.N, 128), info, stream);
+        return Launch<dg::kTN, 256, 5, 2, kF32>::run(ma, mb, p, p.G * ceil_div(p.M, 256) * ceil_div(p.N, 256), info, stream);
+    return Launch<dg::kTN, 128, 5, 1, kF32>::run(ma, mb, p, p.G * ceil_div(p.M, 128) * ceil_div(p.N, 128), info, stream);
 }
 
 }  // namespace

@@ -28,15 +28,15 @@
 //     so the MMAs of the blocks before it run meanwhile.
 //
 // Output.  A lane holds one row of the accumulator; stored straight from there,
-// each instruction touches 32 lines (wgrad of 64 experts, 62 tokens each, 1000 x
-// 2112, BF16: 174 us, against 46 for its bytes).  So a warp gathers 32 x 32 boxes in
-// shared memory and TMA stores write them, clipped at N (and at M, kTN).  Boxes that
-// cross an expert's last row (kNT, kNN) and sums added to d are stored by the lanes.
+// each instruction touches 32 lines (weight gradient of 64 experts, 62 tokens each,
+// 1000 x 2112, BF16: 174 us, against 46 for its bytes).  So a warp turns 32 x 32
+// boxes around in shared memory and stores runs of a row.
 //
 // Roles: warp 0 producer (TMA), warp 1 TMEM and MMA issue, warp 2 clears ragged
-// token rows (kTN), warps 4..11 epilogue: warp w drains TMEM lanes 32 (w % 4),
-// columns of half (w - 4) / 4.  Persistent; two accumulators in rotation, so
-// the next tile's MMAs overlap this tile's stores.
+// token rows (kTN), warps 4.. epilogue: warp w drains TMEM lanes 32 (w % 4), columns
+// of half (w / 4 - 1) % 2.  Persistent; two accumulators in rotation, so the next
+// tile's MMAs overlap this tile's stores, and a group of 8 epilogue warps for each,
+// so that short tiles (few tokens, kTN; short K) store two at a time.
 //
 // CTA pairs (kCtaGroup == 2): 256 x kBN tiles, each CTA stages its 128 rows of
 // A and half of B's columns.  Single CTAs take over where experts have few
@@ -59,7 +59,9 @@ namespace dg {
 
 enum RaggedDir : int { kNT = 0, kNN = 1, kTN = 2 };
 
-constexpr int kRaggedThreads = 384;
+// 4 warps that load, multiply and clear rows, and 8 warps for each accumulator in
+// rotation; two-level FP32 sums take one such group, with more registers
+__host__ __device__ constexpr int ragged_threads(bool f32) { return f32 ? 384 : 640; }
 constexpr int kRaggedBlockK = 64;
 constexpr int kRaggedBand = 8;        // row blocks per L2 raster band
 constexpr int kSegBlocks = 8;         // K-blocks per accumulator segment, FP32 weight gradient
@@ -89,11 +91,10 @@ struct RaggedSmem {
     static constexpr int kMiscOffset = kBarOffset + kNumBars * 8;   // tmem addr, abort flag
     static constexpr int kOffsOffset = (kMiscOffset + 16 + 15) / 16 * 16;
     static constexpr int kPrefixOffset = kOffsOffset + (kMaxGroups + 1) * 4;
-    // epilogue: boxes of 32 rows by 32 columns, 4 KB for each of the 8 warps
+    // epilogue: 32 rows by 32 columns for each of its warps
     static constexpr int kBoxBytes = 32 * 32 * (kF32 ? 4 : 2);
-    static constexpr int kBoxes = 4096 / kBoxBytes;
     static constexpr int kOutOffset = (kPrefixOffset + (kMaxGroups + 1) * 4 + 1023) / 1024 * 1024;
-    static constexpr int kUsed = kOutOffset + 8 * 4096;
+    static constexpr int kUsed = kOutOffset + (ragged_threads(kF32) / 32 - 4) * kBoxBytes;
     static constexpr int kAlloc = (kUsed + 1024 > kMinSmem) ? kUsed + 1024 : kMinSmem;
     static constexpr int kTmemCols = kAccBufs * kBN <= 128 ? 128 : kAccBufs * kBN <= 256 ? 256 : 512;
     static_assert(kBN == 64 || kBN == 128 || kBN == 256, "tile N");
@@ -120,7 +121,7 @@ __host__ __device__ constexpr uint32_t ragged_idesc(int m, int n, bool a_mn, boo
 }
 
 struct RaggedTile {
-    int g;
+    int g = 0;     // in: where the search begins
     int row0;      // kNT, kNN: first token row of the tile (in the buffer); kTN: first output row
     int row_end;   // exclusive bound of its valid rows
     int n0;
@@ -136,25 +137,31 @@ struct RaggedMap {
         const int rows = kDir == kTN ? p.M : offs[g + 1] - offs[g];
         return (rows + kRows - 1) / kRows;
     }
+    // n / d by a reciprocal, put right by a step (small n; the division's latency is in
+    // every role's way once a tile)
+    __device__ static unsigned quotient(unsigned n, unsigned d) {
+        if (n >= (1u << 22)) return n / d;
+        unsigned q = static_cast<unsigned>(__fdividef(static_cast<float>(n), static_cast<float>(d)));
+        if (q * d > n) --q;
+        if (n - q * d >= d) ++q;
+        return q;
+    }
     __device__ static int count(const RaggedParams &p, const int *prefix) { return prefix[p.G]; }
 
     __device__ static void decode(int t, const RaggedParams &p, const int *offs, const int *prefix,
                                   RaggedTile &tl) {
-        int lo = 0, hi = p.G - 1;                     // last g with prefix[g] <= t
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (prefix[mid] <= t) lo = mid; else hi = mid - 1;
-        }
-        const int g = lo, local = t - prefix[g];
-        const int nb = (p.N + kBN - 1) / kBN;
-        const int rb = row_blocks(p, offs, g);
-        const int per_band = kRaggedBand * nb;
-        const int band = local / per_band;
-        const int width = min(kRaggedBand, rb - band * kRaggedBand);
-        const int in_band = local - band * per_band;
-        const int row = (band * kRaggedBand + in_band % width) * kRows;
-        tl.g = g;
-        tl.n0 = in_band / width * kBN;
+        while (prefix[tl.g + 1] <= t) ++tl.g;          // tiles come in order: on from the last one's expert
+        const int g = tl.g;
+        const unsigned local = t - prefix[g];
+        const unsigned nb = (p.N + kBN - 1) / kBN;
+        const unsigned rb = row_blocks(p, offs, g);
+        const unsigned per_band = kRaggedBand * nb;
+        const unsigned band = rb <= kRaggedBand ? 0 : quotient(local, per_band);
+        const unsigned width = min(static_cast<unsigned>(kRaggedBand), rb - band * kRaggedBand);
+        const unsigned in_band = local - band * per_band;
+        const unsigned col = quotient(in_band, width);
+        const int row = static_cast<int>(band * kRaggedBand + in_band - col * width) * kRows;
+        tl.n0 = static_cast<int>(col) * kBN;
         const int tokens = offs[g + 1] - offs[g];
         if (kDir == kTN) {
             tl.row0 = row;
@@ -175,40 +182,22 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// Eight consecutive columns of one output row, 16-byte aligned (32 for FP32).
-template <bool kF32>
-__device__ __forceinline__ void store8(void *d, size_t index, const float *v, bool accumulate) {
-    if constexpr (kF32) {
-        float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(d) + index);
-        float4 a = make_float4(v[0], v[1], v[2], v[3]), b = make_float4(v[4], v[5], v[6], v[7]);
-        if (accumulate) {
-            const float4 x = o[0], y = o[1];
-            a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
-            b.x += y.x; b.y += y.y; b.z += y.z; b.w += y.w;
-        }
-        o[0] = a;
-        o[1] = b;
-    } else {
-        uint4 *o = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(d) + index);
-        float s[8];
+// Adds eight columns to a row of BF16: widened exactly, added in FP32, rounded once.
+__device__ __forceinline__ void add8(__nv_bfloat16 *d, const float *v) {
+    uint4 *o = reinterpret_cast<uint4 *>(d);
+    const uint4 x = *o;
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    float s[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s[j] = v[j];
-        if (accumulate) {                       // BF16 is widened exactly, added in FP32, rounded once
-            const uint4 x = *o;
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                s[2 * j] += __uint_as_float(w[j] << 16);
-                s[2 * j + 1] += __uint_as_float(w[j] & 0xFFFF0000u);
-            }
-        }
-        *o = make_uint4(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]), pack_bf16x2(s[4], s[5]),
-                        pack_bf16x2(s[6], s[7]));
+    for (int j = 0; j < 4; ++j) {
+        s[2 * j] = v[2 * j] + __uint_as_float(w[j] << 16);
+        s[2 * j + 1] = v[2 * j + 1] + __uint_as_float(w[j] & 0xFFFF0000u);
     }
+    *o = make_uint4(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]), pack_bf16x2(s[4], s[5]), pack_bf16x2(s[6], s[7]));
 }
 
-// 32 columns of this lane's row into a warp's box of 32 rows, in the order of the
-// TMA store's swizzle (64 bytes a row for BF16, 128 for FP32).
+// 32 columns of this lane's row into a warp's box of 32 rows, its 16-byte pieces
+// permuted by the row against bank conflicts ...
 template <bool kF32>
 __device__ __forceinline__ void stage32(uint8_t *box, int lane, const float *v) {
     if constexpr (kF32) {
@@ -225,12 +214,51 @@ __device__ __forceinline__ void stage32(uint8_t *box, int lane, const float *v) 
     }
 }
 
+// ... and from there to memory, runs of 64 (BF16) or 128 bytes of a row: `rows` of
+// them exist, of `cols` columns (a multiple of 8).  d: this lane's 16 bytes of the
+// first row that it stores (unstage_row, unstage_col), step: between its rows.
+template <bool kF32>
+__device__ __forceinline__ int unstage_row(int lane) { return kF32 ? lane / 8 : lane / 4; }
+template <bool kF32>
+__device__ __forceinline__ int unstage_col(int lane) { return kF32 ? lane % 8 * 4 : lane % 4 * 8; }
+template <bool kF32>
+__device__ __forceinline__ void unstage32(const uint8_t *box, int lane, uint8_t *d, size_t step, int rows, int cols, bool add) {
+    constexpr int kPieces = kF32 ? 8 : 4;               // 16-byte pieces of a row
+    constexpr int kRowsAt = 32 / kPieces;
+    const int r0 = unstage_row<kF32>(lane), piece = lane % kPieces;
+    uint4 v[kPieces];
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+        const int r = r0 + i * kRowsAt;
+        v[i] = *reinterpret_cast<const uint4 *>(box + (kF32 ? r * 128 + ((piece ^ (r & 7)) << 4)
+                                                            : r * 64 + ((piece ^ ((r >> 1) & 3)) << 4)));
+    }
+    if (unstage_col<kF32>(lane) >= cols) return;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+        if (r0 + i * kRowsAt < rows) {
+            if constexpr (kF32) {
+                float4 f = make_float4(__uint_as_float(v[i].x), __uint_as_float(v[i].y), __uint_as_float(v[i].z),
+                                       __uint_as_float(v[i].w));
+                if (add) {
+                    const float4 x = *reinterpret_cast<const float4 *>(d);
+                    f.x += x.x; f.y += x.y; f.z += x.z; f.w += x.w;
+                }
+                *reinterpret_cast<float4 *>(d) = f;
+            } else {
+                *reinterpret_cast<uint4 *>(d) = v[i];
+            }
+        }
+        d += step;
+    }
+}
+
 // tm_a, tm_b: see the operand table above (kNT, kNN single-CTA: A boxes of 32 rows).
 // tm_d: boxes of 32 columns by 32 rows of D [groups][rows][N] (kTN: one group per expert).
 template <int kDir, int kBN, int kStages, int kCtaGroup, bool kF32>
-__global__ void __launch_bounds__(kRaggedThreads, 1)
+__global__ void __launch_bounds__(ragged_threads(kF32), 1)
 ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
-                   const __grid_constant__ CUtensorMap tm_d, const RaggedParams p) {
+                   const RaggedParams p) {
     using L = RaggedSmem<kDir, kBN, kStages, kCtaGroup, kF32>;
     using TM = RaggedMap<kDir, kBN, kCtaGroup>;
     static_assert(!kF32 || kDir == kTN, "FP32 output: weight gradient");
@@ -268,7 +296,6 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
     if (threadIdx.x == 0) {
         ptx::prefetch_tmap(&tm_a);
         ptx::prefetch_tmap(&tm_b);
-        ptx::prefetch_tmap(&tm_d);
         for (int i = 0; i < kStages; ++i) {
             // kTN: one arrival per CTA (its producer, or its row-clearing warp)
             ptx::mbar_init(full_bar(i), kDir == kTN ? kCtaGroup : 1);
@@ -284,23 +311,39 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
         ptx::fence_mbar_init();
     }
     if (warp == kEpiWarp0) {
-        // offsets as the tiles use them: clamped to [0, T] and made non-decreasing
+        // offsets as the tiles use them: clamped to [0, T] and made non-decreasing.  Four
+        // of them a lane, so that their loads are in flight together.
         int run = 0;
-        for (int base = 0; base <= p.G; base += 32) {
-            const int i = base + lane;
-            const int raw = i <= p.G ? __ldg(p.offsets + i) : 0;
-            int v = min(max(raw, 0), p.T);
+        for (int base = 0; base <= p.G; base += 128) {
+            int raw[4], v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int i = base + 4 * lane + j;
+                raw[j] = i <= p.G ? __ldg(p.offsets + i) : 0;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                v[j] = min(max(raw[j], 0), p.T);
+                if (j) v[j] = max(v[j], v[j - 1]);
+            }
+            int incl = v[3];
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int u = __shfl_up_sync(0xffffffffu, v, o);
-                if (lane >= o) v = max(v, u);
+                const int u = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl = max(incl, u);
             }
-            v = max(v, run);
-            if (i <= p.G) {
-                offs[i] = v;
-                if (v != raw) record_status(p.status, kStatusInvalid, kSiteBadOffsets);
+            int before = __shfl_up_sync(0xffffffffu, incl, 1);
+            before = max(run, lane ? before : 0);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int i = base + 4 * lane + j;
+                v[j] = max(v[j], before);
+                if (i <= p.G) {
+                    offs[i] = v[j];
+                    if (v[j] != raw[j]) record_status(p.status, kStatusInvalid, kSiteBadOffsets);
+                }
             }
-            run = __shfl_sync(0xffffffffu, v, 31);
+            run = max(run, __shfl_sync(0xffffffffu, incl, 31));
         }
         __syncwarp();
         // exclusive prefix of tiles per expert
@@ -348,8 +391,8 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
                 uint32_t phase = 0, tail_phase = 0, tail_armed = 0;   // a bit per stage
                 long long issued = 0;
                 bool ok = (p.debug_flags & kDebugProducerIdle) == 0;
+                RaggedTile tl;
                 for (int t = t_first; ok && t < num_tiles; t += t_step) {
-                    RaggedTile tl;
                     TM::decode(t, p, offs, prefix, tl);
                     // kNT, kNN: rows of A that this CTA loads, in boxes of 32 (single CTAs) or 128
                     const int a_boxes = (kDir != kTN && !kPair) ? (min(tl.row_end - tl.row0, kTileX) + 31) / 32 : 0;
@@ -435,11 +478,13 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
                 const uint32_t idesc = ragged_idesc(kTileX * kCtaGroup, kBN, kAMn, kBMn);
                 constexpr uint32_t kStepA = kAMn ? 2048 >> 4 : 32 >> 4;   // 16 reduced indices
                 constexpr uint32_t kStepB = kBMn ? 2048 >> 4 : 32 >> 4;
+                RaggedTile tl;
                 for (int t = t_first; ok && t < num_tiles; t += t_step) {
-                    RaggedTile tl;
                     TM::decode(t, p, offs, prefix, tl);
-                    const int seg = kPromote ? kSegBlocks : tl.num_kb;
-                    for (int kb0 = 0; ok && kb0 < tl.num_kb; kb0 += seg) {
+                    // one accumulator for the tile (nothing in it for an expert without tokens), or
+                    // one for each segment
+                    const int seg = kPromote ? kSegBlocks : max(tl.num_kb, 1);
+                    for (int kb0 = 0; ok && kb0 < max(tl.num_kb, 1); kb0 += seg) {
                         if (!wait(tempty_bar(buf), tphase ^ 1u, kSiteMmaTmemEmpty)) { ok = false; break; }
                         ptx::tc_fence_after();
                         const uint32_t dtm = tmem_base + static_cast<uint32_t>(buf * kBN);
@@ -447,7 +492,6 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
                         for (int kb = kb0; kb < kb1; ++kb) {
                             if (!wait(full_bar(stage), phase, kSiteMmaFull)) { ok = false; break; }
                             const bool last = kDir == kTN && kb == tl.num_kb - 1;
-                            if (kDir == kTN && kPair && last) ptx::fence_acq_rel_cluster();   // the peer's cleared rows
                             ptx::tc_fence_after();
                             const uint32_t sa = s_base + stage * L::kStageBytes;
                             const uint64_t da = kAMn ? sw128_mn_desc(sa) : sw128_desc(sa);
@@ -480,8 +524,8 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
             // ======================================================== clears ragged token rows
             long long block = 0;                  // K-blocks of the tiles before
             uint32_t tail_phase = 0;              // a bit per stage
+            RaggedTile tl;
             for (int t = t_first; t < num_tiles; t += t_step) {
-                RaggedTile tl;
                 TM::decode(t, p, offs, prefix, tl);
                 block += tl.num_kb;
                 if (tl.num_kb == 0 || (tl.tail & 15) == 0) continue;
@@ -493,23 +537,34 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
                 const int rows = 16 - (tl.tail & 15);
                 constexpr int kBoxes = 2 + L::kBCols / 64;
                 uint8_t *base = smem + stage * L::kStageBytes + tl.tail * 128;
-                for (int i = lane; i < kBoxes * rows * 8; i += 32) {
-                    const int box = i / (rows * 8), at = i - box * rows * 8;
-                    *reinterpret_cast<uint4 *>(base + box * 8192 + at * 16) = make_uint4(0u, 0u, 0u, 0u);
-                }
-                ptx::fence_proxy_async_smem();    // the MMAs read through the async proxy
+                for (int i = lane; i < rows * 8; i += 32)
+#pragma unroll
+                    for (int box = 0; box < kBoxes; ++box)
+                        *reinterpret_cast<uint4 *>(base + box * 8192 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+                // The MMAs read through the async proxy, each CTA's tensor core its own
+                // shared memory: the fence has the zeros there before the arrival leaves.
+                // (An arrival that also releases them at cluster scope waits for the
+                // epilogue's stores in flight as well, 2500 cycles a tile.)
+                ptx::fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive_cluster(leader_addr(full_bar(stage)));
+                if (lane == 0) {
+                    if (kPair && !mma_cta) ptx::mbar_arrive_remote(leader_addr(full_bar(stage)));
+                    else ptx::mbar_arrive(full_bar(stage));
+                }
             }
         }
     } else {
         // ============================================================ epilogue
         if constexpr (kRebalance) ptx::regs_inc<kRegsPromo>();
         const int quarter = warp & 3;
-        const int half = (warp - kEpiWarp0) >> 2;
-        const int lrow = pair_rank * kTileX + quarter * 32 + lane;
-        uint8_t *out = smem + L::kOutOffset + (warp - kEpiWarp0) * 4096;
-        int buf = 0, out_buf = 0;
+        const int half = ((warp - kEpiWarp0) >> 2) & 1;
+        const int group = (warp - kEpiWarp0) >> 3;          // of the accumulators' rotation (FP32: one group for both)
+        const int wrow = pair_rank * kTileX + quarter * 32;  // the warp's first row in a tile
+        uint8_t *out = smem + L::kOutOffset + (warp - kEpiWarp0) * L::kBoxBytes;
+        constexpr int kElem = kF32 ? 4 : 2;
+        const size_t step = static_cast<size_t>(p.N) * kElem * (kF32 ? 4 : 8);   // between a lane's stored rows
+        const bool add = kDir == kTN && p.accumulate;
+        int buf = group;
         uint32_t tphase = 0;
         bool ok = true;
         auto release = [&]() {
@@ -520,93 +575,81 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
                 if (kPair && !mma_cta) ptx::mbar_arrive_remote(leader_addr(tempty_bar(buf)));
                 else ptx::mbar_arrive(tempty_bar(buf));
             }
-            if (++buf == kAccBufs) { buf = 0; tphase ^= 1u; }
+            if (kPromote) buf ^= 1;
+            if (!kPromote || buf == 0) tphase ^= 1u;
         };
-        for (int t = t_first; ok && t < num_tiles; t += t_step) {
-            RaggedTile tl;
+        RaggedTile tl;
+        const int e_step = kPromote ? t_step : 2 * t_step;
+        for (int t = t_first + group * t_step; ok && t < num_tiles; t += e_step) {
             TM::decode(t, p, offs, prefix, tl);
-            const int row = tl.row0 + lrow;
-            const bool row_ok = row < tl.row_end;
-            const size_t base = (kDir == kTN ? static_cast<size_t>(tl.g) * p.M + row : static_cast<size_t>(row)) *
-                                static_cast<size_t>(p.N);
+            const int rows = tl.row_end - (tl.row0 + wrow);        // of the warp's 32
             const int c0 = tl.n0 + half * kHalf;
-            const bool add = kDir == kTN && p.accumulate;
-            // the warp's 32 rows as a box: clipped by the map (kTN) or inside the expert
-            const int box_row = tl.row0 + pair_rank * kTileX + quarter * 32;
-            const bool boxed = !add && (kDir == kTN ? box_row < tl.row_end : box_row + 32 <= tl.row_end);
+            const size_t row0 = (kDir == kTN ? static_cast<size_t>(tl.g) * p.M : 0) + tl.row0 + wrow;
+            uint8_t *dst = static_cast<uint8_t *>(p.d) +
+                           ((row0 + unstage_row<kF32>(lane)) * p.N + c0 + unstage_col<kF32>(lane)) * kElem;
             auto put = [&](int c, const float *v) {      // columns c0 + c .. + 31 of this lane's row
-                if (boxed) {
-                    if (c0 + c < p.N) {
-                        if (lane == 0) {           // what this box held before has been read
-                            if (L::kBoxes == 2) ptx::bulk_wait_read1();
-                            else ptx::bulk_wait_read0();
-                        }
-                        __syncwarp();
-                        uint8_t *box = out + (out_buf ? L::kBoxBytes : 0);
-                        stage32<kF32>(box, lane, v);
-                        ptx::fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) {
-                            ptx::tma_store_3d(&tm_d, ptx::smem_u32(box), c0 + c, box_row, kDir == kTN ? tl.g : 0);
-                            ptx::bulk_commit();
-                        }
-                        out_buf ^= L::kBoxes - 1;
-                    }
-                } else if (row_ok) {
+                if (c0 + c >= p.N || rows <= 0) return;
+                if (kDir == kTN && !kF32 && add) {       // BF16 is added in FP32: before it is rounded
+                    if (lane < rows)
 #pragma unroll
-                    for (int j = 0; j < 32; j += 8)
-                        if (c0 + c + j < p.N) store8<kF32>(p.d, base + c0 + c + j, v + j, add);
+                        for (int j = 0; j < 32; j += 8)
+                            if (c0 + c + j < p.N)
+                                add8(static_cast<__nv_bfloat16 *>(p.d) + (row0 + lane) * p.N + c0 + c + j, v + j);
+                    return;
                 }
+                stage32<kF32>(out, lane, v);
+                __syncwarp();
+                unstage32<kF32>(out, lane, dst + c * kElem, step, rows, p.N - c0 - c, add);
+                __syncwarp();
             };
-            if (tl.num_kb == 0) {                  // kTN, an expert without tokens
-                if (!add) {
-                    float zero[32];
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) zero[j] = 0.f;
-#pragma unroll 1
-                    for (int c = 0; c < kHalf; c += 32) put(c, zero);
-                }
-                continue;
-            }
             if constexpr (kPromote) {
                 float acc[kHalf];
 #pragma unroll
                 for (int j = 0; j < kHalf; ++j) acc[j] = 0.f;
-                for (int kb0 = 0; kb0 < tl.num_kb; kb0 += kSegBlocks) {
+                for (int kb0 = 0; kb0 < max(tl.num_kb, 1); kb0 += kSegBlocks) {
                     if (!wait(tfull_bar(buf), tphase, kSitePromoFull)) { ok = false; break; }
                     ptx::tc_fence_after();
                     const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
                                            static_cast<uint32_t>(buf * kBN + half * kHalf);
+                    if (tl.num_kb > 0) {
 #pragma unroll
-                    for (int c = 0; c < kHalf; c += 16) {
-                        float v[16];
-                        ptx::tmem_ld16(taddr + c, v);
-                        ptx::tmem_wait_ld();
+                        for (int c = 0; c < kHalf; c += 16) {
+                            float v[16];
+                            ptx::tmem_ld16(taddr + c, v);
+                            ptx::tmem_wait_ld();
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) acc[c + j] += v[j];
+                            for (int j = 0; j < 16; ++j) acc[c + j] += v[j];
+                        }
                     }
                     release();
                 }
                 if (!ok) break;
+                if (tl.num_kb > 0 || !add) {
 #pragma unroll
-                for (int c = 0; c < kHalf; c += 32) put(c, acc + c);
+                    for (int c = 0; c < kHalf; c += 32) put(c, acc + c);
+                }
             } else {
                 if (!wait(tfull_bar(buf), tphase, kSitePromoFull)) { ok = false; break; }
                 ptx::tc_fence_after();
                 const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
                                        static_cast<uint32_t>(buf * kBN + half * kHalf);
+                if (tl.num_kb > 0 || !add) {
 #pragma unroll 1
-                for (int c = 0; c < kHalf; c += 32) {
-                    float v[32];
-                    ptx::tmem_ld32p(taddr + c, v);
-                    ptx::tmem_wait_ld();
-                    put(c, v);
+                    for (int c = 0; c < kHalf; c += 32) {
+                        float v[32];
+                        if (kDir != kTN || tl.num_kb > 0) {
+                            ptx::tmem_ld32p(taddr + c, v);
+                            ptx::tmem_wait_ld();
+                        } else {                           // an expert without tokens
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) v[j] = 0.f;
+                        }
+                        put(c, v);
+                    }
                 }
                 release();
             }
         }
-        if (lane == 0) ptx::bulk_wait0();          // never leave with stores reading shared memory
-        __syncwarp();
     }
 
     // ---------------------------------------------------------------- teardown
