@@ -127,23 +127,25 @@ def _th():
 
 def _stream_handle(stream) -> Optional[int]:
     if stream is None:
-        torch = _th()
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        c = _th()._C
+        raw = getattr(c, "_cuda_getCurrentRawStream", None)
         if raw is not None:
-            return raw(torch.cuda.current_device())
-        stream = torch.cuda.current_stream()
+            return raw(c._cuda_getDevice())
+        stream = _th().cuda.current_stream()
     return stream.cuda_stream
 
 
 def _req(t, dtype, name, ndim=None):
-    if not isinstance(t, _th().Tensor) or not t.is_cuda:
+    if not isinstance(t, (_torch or _th()).Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if ndim is not None and t.dim() not in ((ndim,) if isinstance(ndim, int) else ndim):
-        raise ValueError(f"{name} has {t.dim()} dims")
+    if ndim is not None:
+        dims = t.dim()
+        if dims != ndim and (isinstance(ndim, int) or dims not in ndim):
+            raise ValueError(f"{name} has {dims} dims")
     return t.data_ptr()
 
 

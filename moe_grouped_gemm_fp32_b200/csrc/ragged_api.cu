@@ -129,9 +129,14 @@ dg_status_t m_grouped(const void *a, const void *b, void *d, const int32_t *offs
     if ((st = device_info(&info)) != DG_SUCCESS) return st;
     if (T == 0) return DG_SUCCESS;
     const dg::RaggedParams p = ragged_params(d, offsets, T, 0, N, K, G, 0, info);
-    // 256-row CTA pairs where an expert has 128 rows or more on average
-    const bool pair = N > 128 && T >= 256 && T / used >= 128;
-    const int bn = pair ? 256 : ceil_div(N, 128) * used >= info->num_sms ? 128 : 64;
+    // 256-row CTA pairs where an expert has 128 rows or more on average and there are a
+    // few of their tiles: 8 experts of 256 rows, 1024 x 1024: 32 pair tiles 13.4 us, 128
+    // single ones 17.0; one expert of 512 rows: 8 pair tiles 10.9 us, 64 single ones 8.5.
+    // Tiles 64 wide where 128 would leave SMs without one.
+    const long long pair_tiles = ceil_div(T, 256) * ceil_div(N, 256);
+    const bool pair = N > 128 && T / used >= 128 && 8 * pair_tiles >= info->num_sms;
+    const long long row_blocks = ceil_div(T, 128) > used ? ceil_div(T, 128) : used;
+    const int bn = pair ? 256 : ceil_div(N, 128) * row_blocks >= info->num_sms ? 128 : 64;
     CUtensorMap ma, mb;
     if ((st = make_kmajor_map(&ma, a, 2, K, T, 1, pair ? 128 : 32)) != DG_SUCCESS) return st;
     st = kDir == dg::kNT ? make_kmajor_map(&mb, b, 2, K, N, G, pair ? bn / 2 : bn)

@@ -168,31 +168,65 @@ __device__ __forceinline__ bool find_expert(const W4Params &p, int z, bool recor
                                             int &end) {
     int run = 0, seen = 0;
     bool found = false;
-    for (int base = 0; base <= p.G; base += 32) {      // offset i closes expert i - 1
-        const int i = base + lane;
-        const int raw = i <= p.G ? __ldg(p.offsets + i) : 0;
-        int v = min(max(raw, 0), p.M);
+    for (int base = 0; base <= p.G; base += 128) {      // four offsets a lane, their loads in flight together
+        int raw[4], v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int i = base + 4 * lane + j;
+            raw[j] = i <= p.G ? __ldg(p.offsets + i) : 0;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[j] = min(max(raw[j], 0), p.M);
+            if (j) v[j] = max(v[j], v[j - 1]);
+        }
+        int incl = v[3];
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(0xffffffffu, v, o);
-            if (lane >= o) v = max(v, u);
+            const int u = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl = max(incl, u);
         }
-        v = max(v, run);
-        if (record && i <= p.G && v != raw) atomicCAS(p.status, 0u, 1u | (kW4SiteBadOffsets << 8));
-        int before = __shfl_up_sync(0xffffffffu, v, 1);
-        if (lane == 0) before = run;
-        const bool has = i >= 1 && i <= p.G && v > before;
-        const unsigned mask = __ballot_sync(0xffffffffu, has);
-        if (!found && z < seen + __popc(mask)) {
-            const int src = __fns(mask, 0, z - seen + 1);
-            expert = base + src - 1;
-            first = __shfl_sync(0xffffffffu, before, src);
-            end = __shfl_sync(0xffffffffu, v, src);
+        int before = __shfl_up_sync(0xffffffffu, incl, 1);
+        before = max(run, lane ? before : 0);            // offset base + 4 lane - 1
+        int count = 0, last = before;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {                    // offset i closes expert i - 1
+            const int i = base + 4 * lane + j;
+            v[j] = max(v[j], before);
+            if (record && i <= p.G && v[j] != raw[j]) atomicCAS(p.status, 0u, 1u | (kW4SiteBadOffsets << 8));
+            count += i >= 1 && i <= p.G && v[j] > last;
+            last = v[j];
+        }
+        int upto = count;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += u;
+        }
+        const int rank = z - seen - (upto - count);       // of the expert sought among this lane's
+        const bool here = rank >= 0 && rank < count;
+        int at = 0, from = 0, to = 0, k = 0;
+        last = before;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int i = base + 4 * lane + j;
+            if (i >= 1 && i <= p.G && v[j] > last) {
+                if (k == rank) { at = i - 1; from = last; to = v[j]; }
+                ++k;
+            }
+            last = v[j];
+        }
+        const unsigned mask = __ballot_sync(0xffffffffu, here);
+        if (mask != 0u) {
+            const int src = __ffs(static_cast<int>(mask)) - 1;
+            expert = __shfl_sync(0xffffffffu, at, src);
+            first = __shfl_sync(0xffffffffu, from, src);
+            end = __shfl_sync(0xffffffffu, to, src);
             found = true;
             if (!record) return true;
         }
-        seen += __popc(mask);
-        run = __shfl_sync(0xffffffffu, v, 31);
+        seen += __shfl_sync(0xffffffffu, upto, 31);
+        run = max(run, __shfl_sync(0xffffffffu, incl, 31));
     }
     return found;
 }
