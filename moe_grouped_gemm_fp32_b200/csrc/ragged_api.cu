@@ -28,11 +28,11 @@ dg_status_t check_ragged(const void *a, const void *b, const void *d, const int3
     return DG_SUCCESS;
 }
 
-template <int kDir, int kBN, int kStages, int kCtaGroup, bool kF32>
+template <int kDir, int kBN, int kStages, int kCtaGroup, bool kF32, int kRows = 128>
 struct Launch {
-    using L = dg::RaggedSmem<kDir, kBN, kStages, kCtaGroup, kF32>;
+    using L = dg::RaggedSmem<kDir, kBN, kStages, kCtaGroup, kF32, kRows>;
 
-    static auto kernel() { return dg::ragged_gemm_kernel<kDir, kBN, kStages, kCtaGroup, kF32>; }
+    static auto kernel() { return dg::ragged_gemm_kernel<kDir, kBN, kStages, kCtaGroup, kF32, kRows>; }
 
     static void config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute *attr, int grid, cudaStream_t stream) {
         cfg = {};
@@ -88,8 +88,8 @@ struct Launch {
         if (st != DG_SUCCESS) return st;
         const int grid = kCtaGroup * static_cast<int>(tiles < units ? tiles : units);
         if (verbose())
-            std::fprintf(stderr, "[dg] ragged dir=%d bn=%d stages=%d ctas/mma=%d f32=%d grid=%d smem=%d\n", kDir, kBN,
-                         kStages, kCtaGroup, kF32 ? 1 : 0, grid, L::kAlloc);
+            std::fprintf(stderr, "[dg] ragged dir=%d rows=%d bn=%d stages=%d ctas/mma=%d f32=%d grid=%d smem=%d\n", kDir,
+                         kRows, kBN, kStages, kCtaGroup, kF32 ? 1 : 0, grid, L::kAlloc);
         cudaLaunchConfig_t cfg;
         cudaLaunchAttribute attr[1];
         config(cfg, attr, grid, stream);
@@ -124,7 +124,7 @@ dg_status_t m_grouped(const void *a, const void *b, void *d, const int32_t *offs
     dg_status_t st = check_ragged(a, b, d, offsets, T, N, K, G);
     if (st != DG_SUCCESS) return st;
     const int used = T < G ? T : G;              // experts that can have a row
-    if ((ceil_div(T, 128) + used) * ceil_div(N, 64) > kMaxInt) return DG_ERR_UNSUPPORTED_SHAPE;
+    if ((ceil_div(T, 32) + used) * ceil_div(N, 64) > kMaxInt) return DG_ERR_UNSUPPORTED_SHAPE;
     const DeviceInfo *info = nullptr;
     if ((st = device_info(&info)) != DG_SUCCESS) return st;
     if (T == 0) return DG_SUCCESS;
@@ -132,18 +132,24 @@ dg_status_t m_grouped(const void *a, const void *b, void *d, const int32_t *offs
     // 256-row CTA pairs where an expert has 128 rows or more on average and there are a
     // few of their tiles: 8 experts of 256 rows, 1024 x 1024: 32 pair tiles 13.4 us, 128
     // single ones 17.0; one expert of 512 rows: 8 pair tiles 10.9 us, 64 single ones 8.5.
-    // Tiles 64 wide where 128 would leave SMs without one.
+    // Thin tiles of 32 rows where experts have 16 or fewer on average (19 rows, 520 x
+    // 2048: 12.9 us in tiles of 128 rows, 18.6 in thin ones, of which some experts then
+    // need several).  Tiles 64 wide where 128 would leave SMs without one.
     const long long pair_tiles = ceil_div(T, 256) * ceil_div(N, 256);
     const bool pair = N > 128 && T / used >= 128 && 8 * pair_tiles >= info->num_sms;
-    const long long row_blocks = ceil_div(T, 128) > used ? ceil_div(T, 128) : used;
-    const int bn = pair ? 256 : ceil_div(N, 128) * row_blocks >= info->num_sms ? 128 : 64;
+    const bool thin = !pair && T / used <= 16;
+    const int rows = pair ? 256 : thin ? 32 : 128;
+    const long long filled = ceil_div(T, rows) > used ? ceil_div(T, rows) : used;     // row blocks, about
+    const int bn = pair ? 256 : ceil_div(N, 128) * filled >= info->num_sms ? 128 : 64;
     CUtensorMap ma, mb;
     if ((st = make_kmajor_map(&ma, a, 2, K, T, 1, pair ? 128 : 32)) != DG_SUCCESS) return st;
     st = kDir == dg::kNT ? make_kmajor_map(&mb, b, 2, K, N, G, pair ? bn / 2 : bn)
                          : make_kmajor_map(&mb, b, 2, N, K, G, dg::kRaggedBlockK);
     if (st != DG_SUCCESS) return st;
-    const long long tiles = (ceil_div(T, pair ? 256 : 128) + used) * ceil_div(N, bn);
+    const long long tiles = (ceil_div(T, rows) + used) * ceil_div(N, bn);
     if (pair) return Launch<kDir, 256, 5, 2, false>::run(ma, mb, p, tiles, info, stream);
+    if (thin && bn == 128) return Launch<kDir, 128, 9, 1, false, 32>::run(ma, mb, p, tiles, info, stream);
+    if (thin) return Launch<kDir, 64, 7, 1, false, 32>::run(ma, mb, p, tiles, info, stream);
     if (bn == 128) return Launch<kDir, 128, 5, 1, false>::run(ma, mb, p, tiles, info, stream);
     return Launch<kDir, 64, 7, 1, false>::run(ma, mb, p, tiles, info, stream);
 }

@@ -41,7 +41,12 @@
 // CTA pairs (kCtaGroup == 2): 256 x kBN tiles, each CTA stages its 128 rows of
 // A and half of B's columns.  Single CTAs take over where experts have few
 // rows: there A comes in boxes of 32 rows, only those that the expert has, so
-// that weight bytes, not token tiles, fill the memory pipeline.
+// that weight bytes, not token tiles, fill the memory pipeline.  Where experts have
+// a few rows, tiles are thin (kRows 32): a stage keeps 4 KB for A and not 16, and
+// twice as many weight bytes are in flight (64 rows over 16 experts, 4096 x 7168: 156
+// -> 143 us, 98 % of the copy rate).  The MMA still has 128 rows; rows 32 and
+// on read whatever follows in shared memory (B, the next stage, in the middle of
+// being written perhaps) and give accumulator rows that nobody reads.
 //
 // Precision.  The tensor core's FP32 accumulator truncates: measured against 64
 // bits, a sum of 8192 products loses 9e-6 (relative, 2-norm) and 32768 products
@@ -79,12 +84,17 @@ struct RaggedParams {
     int debug_flags;
 };
 
-template <int kDir, int kBN, int kStages, int kCtaGroup, bool kF32>
+template <int kDir, int kBN, int kStages, int kCtaGroup, bool kF32, int kRows>
 struct RaggedSmem {
-    static constexpr int kABytes = kTileX * 128;
+    static constexpr int kABytes = kRows * 128;
     static constexpr int kBCols = kBN / kCtaGroup;            // this CTA's columns of B
     static constexpr int kBBytes = kBCols * 128;
-    static constexpr int kStageBytes = kABytes + kBBytes;
+    // K-blocks of 64 in a stage: two in thin tiles of 64 columns, where few tiles wait on
+    // a block's barriers and issue (0.2 us) rather than on its bytes: 4 rows, 1024 x
+    // 8192, 27.3 -> 21.9 us
+    static constexpr int kSub = kRows == 32 && kBN == 64 ? 2 : 1;
+    static constexpr int kSubBytes = kABytes + kBBytes;
+    static constexpr int kStageBytes = kSub * kSubBytes;
     static constexpr int kAccBufs = 2;
     static constexpr int kBarOffset = kStages * kStageBytes;
     static constexpr int kNumBars = 3 * kStages + 2 * kAccBufs + 1;
@@ -129,9 +139,9 @@ struct RaggedTile {
     int tail;      // kTN: tokens in the last K-block (1..64), 64 elsewhere
 };
 
-template <int kDir, int kBN, int kCtaGroup>
+template <int kDir, int kBN, int kCtaGroup, int kCtaRows>
 struct RaggedMap {
-    static constexpr int kRows = kTileX * kCtaGroup;
+    static constexpr int kRows = kCtaRows * kCtaGroup;
 
     __device__ static int row_blocks(const RaggedParams &p, const int *offs, int g) {
         const int rows = kDir == kTN ? p.M : offs[g + 1] - offs[g];
@@ -255,13 +265,17 @@ __device__ __forceinline__ void unstage32(const uint8_t *box, int lane, uint8_t 
 
 // tm_a, tm_b: see the operand table above (kNT, kNN single-CTA: A boxes of 32 rows).
 // tm_d: boxes of 32 columns by 32 rows of D [groups][rows][N] (kTN: one group per expert).
-template <int kDir, int kBN, int kStages, int kCtaGroup, bool kF32>
+// kRows: rows of a CTA's tile (32 or 128).
+template <int kDir, int kBN, int kStages, int kCtaGroup, bool kF32, int kRows>
 __global__ void __launch_bounds__(ragged_threads(kF32), 1)
 ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                    const RaggedParams p) {
-    using L = RaggedSmem<kDir, kBN, kStages, kCtaGroup, kF32>;
-    using TM = RaggedMap<kDir, kBN, kCtaGroup>;
+    using L = RaggedSmem<kDir, kBN, kStages, kCtaGroup, kF32, kRows>;
+    using TM = RaggedMap<kDir, kBN, kCtaGroup, kRows>;
     static_assert(!kF32 || kDir == kTN, "FP32 output: weight gradient");
+    static_assert(kRows == kTileX || (kRows == 32 && kDir != kTN && kCtaGroup == 1), "thin tiles: one CTA, K-major A");
+    // a thin tile's A descriptor runs on over 96 rows' bytes that follow its 32
+    static_assert(kTileX * 128 <= L::kStageBytes + (L::kUsed - L::kBarOffset), "A reads stay inside shared memory");
     constexpr bool kPair = kCtaGroup == 2;
     constexpr bool kAMn = kDir == kTN, kBMn = kDir != kNT;
     constexpr int kAccBufs = L::kAccBufs;
@@ -395,11 +409,11 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
                 for (int t = t_first; ok && t < num_tiles; t += t_step) {
                     TM::decode(t, p, offs, prefix, tl);
                     // kNT, kNN: rows of A that this CTA loads, in boxes of 32 (single CTAs) or 128
-                    const int a_boxes = (kDir != kTN && !kPair) ? (min(tl.row_end - tl.row0, kTileX) + 31) / 32 : 0;
-                    const uint32_t bytes = (kDir != kTN && !kPair) ? a_boxes * 4096u + L::kBBytes
+                    const int a_boxes = (kDir != kTN && !kPair) ? (min(tl.row_end - tl.row0, kRows) + 31) / 32 : 0;
+                    const uint32_t bytes = (kDir != kTN && !kPair) ? L::kSub * (a_boxes * 4096u + L::kBBytes)
                                                                    : static_cast<uint32_t>(L::kStageBytes);
                     const int nb0 = tl.n0 + pair_rank * L::kBCols;
-                    for (int kb = 0; kb < tl.num_kb; ++kb) {
+                    for (int kb = 0; kb < tl.num_kb; kb += L::kSub) {
                         if (!wait(empty_bar(stage), phase ^ 1u, kSiteProducerEmpty)) { ok = false; break; }
                         const uint32_t sa = s_base + stage * L::kStageBytes;
                         const uint32_t sb = sa + L::kABytes;
@@ -431,17 +445,22 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
                             for (int i = 0; i < L::kBCols / 64; ++i)
                                 load(sb + i * 8192u, &tm_b, nb0 + 64 * i, tok, 0);
                         } else {
-                            if constexpr (kPair) {
-                                load(sa, &tm_a, k0, tl.row0 + pair_rank * kTileX, 0);
-                            } else {
-                                for (int i = 0; i < a_boxes; ++i)
-                                    load(sa + i * 4096u, &tm_a, k0, tl.row0 + 32 * i, 0);
-                            }
-                            if constexpr (kDir == kNT) {
-                                load(sb, &tm_b, k0, nb0, tl.g);
-                            } else {
-                                for (int i = 0; i < L::kBCols / 64; ++i)
-                                    load(sb + i * 8192u, &tm_b, nb0 + 64 * i, k0, tl.g);
+#pragma unroll
+                            for (int s = 0; s < L::kSub; ++s) {          // (past K: zeros)
+                                const uint32_t a = sa + s * L::kSubBytes, b = a + L::kABytes;
+                                const int k = k0 + s * kRaggedBlockK;
+                                if constexpr (kPair) {
+                                    load(a, &tm_a, k, tl.row0 + pair_rank * kTileX, 0);
+                                } else {
+                                    for (int i = 0; i < a_boxes; ++i)
+                                        load(a + i * 4096u, &tm_a, k, tl.row0 + 32 * i, 0);
+                                }
+                                if constexpr (kDir == kNT) {
+                                    load(b, &tm_b, k, nb0, tl.g);
+                                } else {
+                                    for (int i = 0; i < L::kBCols / 64; ++i)
+                                        load(b + i * 8192u, &tm_b, nb0 + 64 * i, k, tl.g);
+                                }
                             }
                         }
                         ++issued;
@@ -489,20 +508,23 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
                         ptx::tc_fence_after();
                         const uint32_t dtm = tmem_base + static_cast<uint32_t>(buf * kBN);
                         const int kb1 = min(kb0 + seg, tl.num_kb);
-                        for (int kb = kb0; kb < kb1; ++kb) {
+                        for (int kb = kb0; kb < kb1; kb += L::kSub) {
                             if (!wait(full_bar(stage), phase, kSiteMmaFull)) { ok = false; break; }
                             const bool last = kDir == kTN && kb == tl.num_kb - 1;
                             ptx::tc_fence_after();
-                            const uint32_t sa = s_base + stage * L::kStageBytes;
-                            const uint64_t da = kAMn ? sw128_mn_desc(sa) : sw128_desc(sa);
-                            const uint64_t db = kBMn ? sw128_mn_desc(sa + L::kABytes) : sw128_desc(sa + L::kABytes);
                             const int steps = last ? (tl.tail + 15) / 16 : kRaggedBlockK / 16;
 #pragma unroll
-                            for (int k = 0; k < kRaggedBlockK / 16; ++k) {
-                                if (k < steps) {
-                                    const uint32_t acc = (kb > kb0 || k > 0) ? 1u : 0u;
-                                    if constexpr (kPair) ptx::mma_f16_pair(dtm, da + kStepA * k, db + kStepB * k, idesc, acc);
-                                    else ptx::mma_f16(dtm, da + kStepA * k, db + kStepB * k, idesc, acc);
+                            for (int s = 0; s < L::kSub; ++s) {
+                                const uint32_t sa = s_base + stage * L::kStageBytes + s * L::kSubBytes;
+                                const uint64_t da = kAMn ? sw128_mn_desc(sa) : sw128_desc(sa);
+                                const uint64_t db = kBMn ? sw128_mn_desc(sa + L::kABytes) : sw128_desc(sa + L::kABytes);
+#pragma unroll
+                                for (int k = 0; k < kRaggedBlockK / 16; ++k) {
+                                    if (k < steps) {
+                                        const uint32_t acc = (kb > kb0 || s > 0 || k > 0) ? 1u : 0u;
+                                        if constexpr (kPair) ptx::mma_f16_pair(dtm, da + kStepA * k, db + kStepB * k, idesc, acc);
+                                        else ptx::mma_f16(dtm, da + kStepA * k, db + kStepB * k, idesc, acc);
+                                    }
                                 }
                             }
                             if constexpr (kPair) ptx::mma_commit_pair(empty_bar(stage), 0x3);
@@ -582,7 +604,7 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
         const int e_step = kPromote ? t_step : 2 * t_step;
         for (int t = t_first + group * t_step; ok && t < num_tiles; t += e_step) {
             TM::decode(t, p, offs, prefix, tl);
-            const int rows = tl.row_end - (tl.row0 + wrow);        // of the warp's 32
+            const int rows = min(tl.row_end, tl.row0 + pair_rank * kTileX + kRows) - (tl.row0 + wrow);   // of the warp's 32
             const int c0 = tl.n0 + half * kHalf;
             const size_t row0 = (kDir == kTN ? static_cast<size_t>(tl.g) * p.M : 0) + tl.row0 + wrow;
             uint8_t *dst = static_cast<uint8_t *>(p.d) +

@@ -20,7 +20,7 @@ dg_status_t check_w4(const void *x, const void *w, const void *s, const void *z,
     if (M < 0 || N <= 0 || K <= 0 || G <= 0) return DG_ERR_INVALID_VALUE;
     if (group_size != 32 && group_size != 64 && group_size != 128) return DG_ERR_UNSUPPORTED_SHAPE;
     if (K % group_size != 0 || N % 8 != 0 || G > 1024) return DG_ERR_UNSUPPORTED_SHAPE;
-    if (M > 65535 * 32 || K > (1 << 30) || (N + dg::kW4Rows - 1) / dg::kW4Rows > 65535) return DG_ERR_UNSUPPORTED_SHAPE;   // grid.y
+    if (K > (1 << 30) || (N + dg::kW4Rows - 1) / dg::kW4Rows > 65535) return DG_ERR_UNSUPPORTED_SHAPE;   // grid.y
     if (!aligned16(x) || !aligned16(w) || !aligned16(s) || !aligned16(z) || !aligned16(d)) return DG_ERR_MISALIGNED;
     return DG_SUCCESS;
 }
@@ -28,6 +28,7 @@ dg_status_t check_w4(const void *x, const void *w, const void *s, const void *z,
 template <int kGs, int kNT, bool kZeros>
 dg_status_t launch_w4(dg::W4Params p, int split, int runs, cudaStream_t stream) {
     using L = dg::W4Smem<kGs>;
+    if (runs > 65535) return DG_ERR_UNSUPPORTED_SHAPE;      // grid.z
     auto kernel = dg::w4_gemv_kernel<kGs, kNT, kZeros>;
     const int blocks = (p.K + dg::kW4BlockK - 1) / dg::kW4BlockK;
     const int per_cta = (blocks + split - 1) / split;
@@ -64,12 +65,16 @@ dg_status_t launch_w4(dg::W4Params p, int split, int runs, cudaStream_t stream) 
     return e == cudaSuccess ? DG_SUCCESS : cuda_fail(e, "w4_gemv_kernel launch");
 }
 
-// experts: those that can have rows (0: dense, a run of rows for each CTA)
+// runs of `rows` rows that M rows of `experts` experts can make at most
+int runs_of(int M, int experts, int rows) { return experts + (M - experts) / rows; }
+
+// experts: those that can have rows (0: dense)
 template <int kGs, bool kZeros>
 dg_status_t dispatch_tokens(const dg::W4Params &p, int tokens, int experts, int split, cudaStream_t stream) {
-    if (tokens <= 8) return launch_w4<kGs, 1, kZeros>(p, split, experts ? experts : (p.M + 7) / 8, stream);
-    if (tokens <= 16) return launch_w4<kGs, 2, kZeros>(p, split, experts ? experts : (p.M + 15) / 16, stream);
-    return launch_w4<kGs, 4, kZeros>(p, split, experts ? experts : (p.M + 31) / 32, stream);
+    auto runs = [&](int rows) { return experts ? runs_of(p.M, experts, rows) : (p.M + rows - 1) / rows; };
+    if (tokens <= 8) return launch_w4<kGs, 1, kZeros>(p, split, runs(8), stream);
+    if (tokens <= 16) return launch_w4<kGs, 2, kZeros>(p, split, runs(16), stream);
+    return launch_w4<kGs, 4, kZeros>(p, split, runs(32), stream);
 }
 
 template <int kGs>

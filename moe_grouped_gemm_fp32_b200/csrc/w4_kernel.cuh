@@ -64,7 +64,7 @@ struct W4Params {
 };
 
 // K blocks of x and scales staged at once, at most; a multiple of kW4Depth, small
-// enough for four CTAs on an SM
+// enough for five CTAs on an SM (kNT 1; four and three for 2 and 4)
 template <int kNT>
 constexpr int w4_max_chunk() { return kNT == 1 ? 8 : 4; }
 
@@ -161,10 +161,10 @@ __device__ __forceinline__ int x_slot(int c) {
     return c;
 }
 
-// The z-th expert that has rows, its first row and the end of them; false if
-// there are fewer.  Offsets are used clamped to [0, M] and raised to the largest
+// The z-th run of at most run_rows rows of an expert: the expert, the run's first row
+// and its end; false if there are fewer runs.  Offsets are used clamped to [0, M] and raised to the largest
 // before; `record` marks those that were not so.
-__device__ __forceinline__ bool find_expert(const W4Params &p, int z, bool record, int lane, int &expert, int &first,
+__device__ __forceinline__ bool find_expert(const W4Params &p, int run_rows, int z, bool record, int lane, int &expert, int &first,
                                             int &end) {
     int run = 0, seen = 0;
     bool found = false;
@@ -194,7 +194,7 @@ __device__ __forceinline__ bool find_expert(const W4Params &p, int z, bool recor
             const int i = base + 4 * lane + j;
             v[j] = max(v[j], before);
             if (record && i <= p.G && v[j] != raw[j]) atomicCAS(p.status, 0u, 1u | (kW4SiteBadOffsets << 8));
-            count += i >= 1 && i <= p.G && v[j] > last;
+            if (i >= 1 && i <= p.G) count += (v[j] - last + run_rows - 1) / run_rows;
             last = v[j];
         }
         int upto = count;
@@ -211,8 +211,13 @@ __device__ __forceinline__ bool find_expert(const W4Params &p, int z, bool recor
         for (int j = 0; j < 4; ++j) {
             const int i = base + 4 * lane + j;
             if (i >= 1 && i <= p.G && v[j] > last) {
-                if (k == rank) { at = i - 1; from = last; to = v[j]; }
-                ++k;
+                const int runs = (v[j] - last + run_rows - 1) / run_rows;
+                if (rank >= k && rank < k + runs) {
+                    at = i - 1;
+                    from = last + (rank - k) * run_rows;
+                    to = min(v[j], from + run_rows);
+                }
+                k += runs;
             }
             last = v[j];
         }
@@ -233,9 +238,9 @@ __device__ __forceinline__ bool find_expert(const W4Params &p, int z, bool recor
 
 }  // namespace w4
 
-// grid (split, row blocks, experts with rows or runs of 8 kNT tokens), cluster (split, 1, 1)
+// grid (split, row blocks, runs of 8 kNT tokens), cluster (split, 1, 1)
 template <int kGs, int kNT, bool kZeros>
-__global__ void __launch_bounds__(kW4Threads, kNT == 4 ? 3 : 4)
+__global__ void __launch_bounds__(kW4Threads, kNT == 4 ? 3 : kNT == 2 ? 4 : 5)
 w4_gemv_kernel(const W4Params p) {
     using L = W4Smem<kGs>;
     constexpr int kTok = 8 * kNT;
@@ -253,7 +258,7 @@ w4_gemv_kernel(const W4Params p) {
     if (p.offsets) {
         const int z = static_cast<int>(blockIdx.z);
         const bool record = z == 0 && rank == 0 && n0 == 0 && warp == 0;
-        if (!w4::find_expert(p, z, record, lane, expert, first, end)) return;   // the whole cluster: it shares z
+        if (!w4::find_expert(p, kTok, z, record, lane, expert, first, end)) return;   // the whole cluster: it shares z
     }
 
     const int num_blk = (p.K + kW4BlockK - 1) / kW4BlockK;
@@ -285,7 +290,6 @@ w4_gemv_kernel(const W4Params p) {
     for (int i = tid * 16; i < static_cast<int>(x_pitch); i += kW4Threads * 16)
         w4::sts128(zero_row + i, make_uint4(0u, 0u, 0u, 0u));
     if (split > 1) ptx::cluster_arrive_relaxed();   // waited for before the first store into another CTA
-    bool started = split == 1;
 
     // A warp's rows of block `blk`, whose slot `u` is blk - blk0 modulo kW4Depth, from
     // `ahead` bytes past wptr; zeros past K.
@@ -305,184 +309,174 @@ w4_gemv_kernel(const W4Params p) {
         w4::cp_commit();
     };
 
-    for (int m0 = first; m0 < end; m0 += kTok) {
-        const int ntok = min(kTok, end - m0);
-        float acc[2][kNT][4];
+    const int m0 = first, ntok = end - first;
+    float acc[2][kNT][4];
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
+    for (int r = 0; r < 2; ++r)
 #pragma unroll
-            for (int i = 0; i < kNT; ++i)
+        for (int i = 0; i < kNT; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc[r][i][j] = 0.f;
-        // where this lane's rows of x lie: tokens past the expert's read zeros
-        uint32_t xrow[kNT];
+            for (int j = 0; j < 4; ++j) acc[r][i][j] = 0.f;
+    // where this lane's rows of x lie: tokens past the expert's read zeros
+    uint32_t xrow[kNT];
 #pragma unroll
-        for (int n = 0; n < kNT; ++n)
-            xrow[n] = (8 * n + g8 < ntok ? s_base + L::kXOffset + (8 * n + g8) * x_pitch : zero_row) + t4 * 16;
+    for (int n = 0; n < kNT; ++n)
+        xrow[n] = (8 * n + g8 < ntok ? s_base + L::kXOffset + (8 * n + g8) * x_pitch : zero_row) + t4 * 16;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) wptr[i] = wrow[i] + static_cast<size_t>(blk0) * (kW4BlockK / 2);
+    for (int i = 0; i < 4; ++i) wptr[i] = wrow[i] + static_cast<size_t>(blk0) * (kW4BlockK / 2);
 #pragma unroll
-        for (int d = 0; d < kW4Depth; ++d) copy(blk0 + d, d, d * (kW4BlockK / 2));
+    for (int d = 0; d < kW4Depth; ++d) copy(blk0 + d, d, d * (kW4BlockK / 2));
 
-        for (int c0 = blk0; c0 < blk1; c0 += p.chunk) {
-            const int c1 = min(c0 + p.chunk, blk1);
-            if (c0 != blk0) __syncthreads();       // the chunk before has been read
-            // scales and zero points; groups past K: zero
-            for (int i = tid; i < (c1 - c0) * kGroups * 16; i += kW4Threads) {
-                const int j = i >> 4, c = i & 15;
-                if (c * 8 < rows_left) {
-                    const int grp = c0 * kGroups + j;
-                    const bool ok = grp < static_cast<int>(groups);
-                    const size_t at = static_cast<size_t>(ok ? grp : 0) * p.N + c * 8;
-                    w4::cp16(s_base + L::s_offset(p.tok_cap, p.chunk) + j * (kW4Rows * 2) + c * 16, sc + at, ok ? 16u : 0u);
-                    if (kZeros) w4::cp8(s_base + L::z_offset(p.tok_cap, p.chunk) + j * kW4Rows + c * 8, zp + at);
-                }
+    for (int c0 = blk0; c0 < blk1; c0 += p.chunk) {
+        const int c1 = min(c0 + p.chunk, blk1);
+        if (c0 != blk0) __syncthreads();       // the chunk before has been read
+        // scales and zero points; groups past K: zero
+        for (int i = tid; i < (c1 - c0) * kGroups * 16; i += kW4Threads) {
+            const int j = i >> 4, c = i & 15;
+            if (c * 8 < rows_left) {
+                const int grp = c0 * kGroups + j;
+                const bool ok = grp < static_cast<int>(groups);
+                const size_t at = static_cast<size_t>(ok ? grp : 0) * p.N + c * 8;
+                w4::cp16(s_base + L::s_offset(p.tok_cap, p.chunk) + j * (kW4Rows * 2) + c * 16, sc + at, ok ? 16u : 0u);
+                if (kZeros) w4::cp8(s_base + L::z_offset(p.tok_cap, p.chunk) + j * kW4Rows + c * 8, zp + at);
             }
-            w4::cp_commit();
-            // x, 8 values at a time, in the products' order; zeros past K.  Thread: piece
-            // tid % 16 of each block, tokens tid / 16, tid / 16 + 8, ...
-            {
-                const int c = tid & 15;
-                const int have = (p.K - c0 * kW4BlockK - c * 8 + kW4BlockK - 1) / kW4BlockK;   // blocks whose piece lies below K
+        }
+        w4::cp_commit();
+        // x, 8 values at a time, in the products' order; zeros past K.  Thread: piece
+        // tid % 16 of each block, tokens tid / 16, tid / 16 + 8, ...
+        {
+            const int c = tid & 15;
+            const int have = (p.K - c0 * kW4BlockK - c * 8 + kW4BlockK - 1) / kW4BlockK;   // blocks whose piece lies below K
 #pragma unroll
-                for (int n = 0; n < kNT; ++n) {
-                    const int tok = 8 * n + (tid >> 4);
-                    if (tok < ntok) {
-                        const uint4 *src = reinterpret_cast<const uint4 *>(
-                            p.x + static_cast<size_t>(m0 + tok) * p.K + static_cast<size_t>(c0) * kW4BlockK) + c;
-                        uint32_t dst = s_base + L::kXOffset + tok * x_pitch + w4::x_slot<kGs>(c) * 16;
+            for (int n = 0; n < kNT; ++n) {
+                const int tok = 8 * n + (tid >> 4);
+                if (tok < ntok) {
+                    const uint4 *src = reinterpret_cast<const uint4 *>(
+                        p.x + static_cast<size_t>(m0 + tok) * p.K + static_cast<size_t>(c0) * kW4BlockK) + c;
+                    uint32_t dst = s_base + L::kXOffset + tok * x_pitch + w4::x_slot<kGs>(c) * 16;
 #pragma unroll 4
-                        for (int b = 0; b < c1 - c0; ++b) {
-                            const uint4 v = b < have ? __ldg(src + b * 16) : make_uint4(0u, 0u, 0u, 0u);
-                            w4::sts128(dst + b * 256,
-                                       make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
-                                                  __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632)));
-                        }
+                    for (int b = 0; b < c1 - c0; ++b) {
+                        const uint4 v = b < have ? __ldg(src + b * 16) : make_uint4(0u, 0u, 0u, 0u);
+                        w4::sts128(dst + b * 256,
+                                   make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
+                                              __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632)));
                     }
                 }
             }
-            w4::cp_wait<0>();
-            __syncthreads();
-            uint32_t xa[kNT], sa = s_off, za = z_off;
+        }
+        w4::cp_wait<0>();
+        __syncthreads();
+        uint32_t xa[kNT], sa = s_off, za = z_off;
 #pragma unroll
-            for (int n = 0; n < kNT; ++n) xa[n] = xrow[n];
-            // a chunk starts at a multiple of kW4Depth blocks from blk0: block b0 + u lies in slot u
-            for (int b0 = c0; b0 < c1; b0 += kW4Depth) {
+        for (int n = 0; n < kNT; ++n) xa[n] = xrow[n];
+        // a chunk starts at a multiple of kW4Depth blocks from blk0: block b0 + u lies in slot u
+        for (int b0 = c0; b0 < c1; b0 += kW4Depth) {
 #pragma unroll
-                for (int u = 0; u < kW4Depth; ++u) {
-                    if (b0 + u >= c1) break;
-                    w4::cp_wait<kW4Depth - 1>();
-                    __syncwarp();                  // every lane's copies of this block have landed
+            for (int u = 0; u < kW4Depth; ++u) {
+                if (b0 + u >= c1) break;
+                w4::cp_wait<kW4Depth - 1>();
+                __syncwarp();                  // every lane's copies of this block have landed
 #pragma unroll
-                    for (int j = 0; j < kGroups; ++j) {
-                        uint32_t zero[4] = {0x43084308u, 0x43084308u, 0x43084308u, 0x43084308u};
-                        if constexpr (kZeros) {
-                            const uint32_t zb = w4::lds32(za + u * L::kZBlock + j * kW4Rows) & 0x7F7F7F7Fu;
+                for (int j = 0; j < kGroups; ++j) {
+                    uint32_t zero[4] = {0x43084308u, 0x43084308u, 0x43084308u, 0x43084308u};
+                    if constexpr (kZeros) {
+                        const uint32_t zb = w4::lds32(za + u * L::kZBlock + j * kW4Rows) & 0x7F7F7F7Fu;
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) zero[i] = __byte_perm(zb, 0x43u, 0x4040 + i * 0x0101);   // 128 + z
+                        for (int i = 0; i < 4; ++i) zero[i] = __byte_perm(zb, 0x43u, 0x4040 + i * 0x0101);   // 128 + z
+                    }
+                    uint32_t w[4][kWords];
+                    const uint32_t wa = (w_read ^ (j * (64 / kGroups))) + u * kW4WarpBlock;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if constexpr (kGs == 128) {
+                            const uint4 v = w4::lds128(wa + i * 512);
+                            w[i][0] = v.x; w[i][1] = v.y; w[i][2] = v.z; w[i][3] = v.w;
+                        } else if constexpr (kGs == 64) {
+                            const uint2 v = w4::lds64(wa + i * 512);
+                            w[i][0] = v.x; w[i][1] = v.y;
+                        } else {
+                            w[i][0] = w4::lds32(wa + i * 512);
                         }
-                        uint32_t w[4][kWords];
-                        const uint32_t wa = (w_read ^ (j * (64 / kGroups))) + u * kW4WarpBlock;
+                    }
+                    float c[2][kNT][4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            if constexpr (kGs == 128) {
-                                const uint4 v = w4::lds128(wa + i * 512);
-                                w[i][0] = v.x; w[i][1] = v.y; w[i][2] = v.z; w[i][3] = v.w;
-                            } else if constexpr (kGs == 64) {
-                                const uint2 v = w4::lds64(wa + i * 512);
-                                w[i][0] = v.x; w[i][1] = v.y;
-                            } else {
-                                w[i][0] = w4::lds32(wa + i * 512);
-                            }
-                        }
-                        float c[2][kNT][4];
+                    for (int k = 0; k < kWords; ++k) {
+                        uint4 x[kNT];
 #pragma unroll
-                        for (int k = 0; k < kWords; ++k) {
-                            uint4 x[kNT];
+                        for (int n = 0; n < kNT; ++n) x[n] = w4::lds128(xa[n] + u * 256 + (j * kWords + k) * 64);
 #pragma unroll
-                            for (int n = 0; n < kNT; ++n) x[n] = w4::lds128(xa[n] + u * 256 + (j * kWords + k) * 64);
-#pragma unroll
-                            for (int r = 0; r < 2; ++r) {
-                                const uint32_t lo = w[2 * r][k], hi = w[2 * r + 1][k];
-                                const uint32_t zl = zero[2 * r], zh = zero[2 * r + 1];
-                                const uint32_t l0 = w4::codes<0>(lo, bias, zl), l1 = w4::codes<1>(lo, bias, zl),
-                                               l2 = w4::codes<2>(lo, bias, zl), l3 = w4::codes<3>(lo, bias, zl);
-                                const uint32_t h0 = w4::codes<0>(hi, bias, zh), h1 = w4::codes<1>(hi, bias, zh),
-                                               h2 = w4::codes<2>(hi, bias, zh), h3 = w4::codes<3>(hi, bias, zh);
-#pragma unroll
-                                for (int n = 0; n < kNT; ++n) {
-                                    if (k == 0) w4::mma_first(c[r][n], l0, h0, l1, h1, x[n].x, x[n].y);
-                                    else w4::mma(c[r][n], l0, h0, l1, h1, x[n].x, x[n].y);
-                                    w4::mma(c[r][n], l2, h2, l3, h3, x[n].z, x[n].w);
-                                }
-                            }
-                        }
-                        const uint2 sv = w4::lds64(sa + u * L::kSBlock + j * (kW4Rows * 2));
-                        const float s4[4] = {__uint_as_float(sv.x << 16), __uint_as_float(sv.x & 0xFFFF0000u),
-                                             __uint_as_float(sv.y << 16), __uint_as_float(sv.y & 0xFFFF0000u)};
-#pragma unroll
-                        for (int r = 0; r < 2; ++r)
+                        for (int r = 0; r < 2; ++r) {
+                            const uint32_t lo = w[2 * r][k], hi = w[2 * r + 1][k];
+                            const uint32_t zl = zero[2 * r], zh = zero[2 * r + 1];
+                            const uint32_t l0 = w4::codes<0>(lo, bias, zl), l1 = w4::codes<1>(lo, bias, zl),
+                                           l2 = w4::codes<2>(lo, bias, zl), l3 = w4::codes<3>(lo, bias, zl);
+                            const uint32_t h0 = w4::codes<0>(hi, bias, zh), h1 = w4::codes<1>(hi, bias, zh),
+                                           h2 = w4::codes<2>(hi, bias, zh), h3 = w4::codes<3>(hi, bias, zh);
 #pragma unroll
                             for (int n = 0; n < kNT; ++n) {
-                                acc[r][n][0] = fmaf(s4[2 * r], c[r][n][0], acc[r][n][0]);
-                                acc[r][n][1] = fmaf(s4[2 * r], c[r][n][1], acc[r][n][1]);
-                                acc[r][n][2] = fmaf(s4[2 * r + 1], c[r][n][2], acc[r][n][2]);
-                                acc[r][n][3] = fmaf(s4[2 * r + 1], c[r][n][3], acc[r][n][3]);
+                                if (k == 0) w4::mma_first(c[r][n], l0, h0, l1, h1, x[n].x, x[n].y);
+                                else w4::mma(c[r][n], l0, h0, l1, h1, x[n].x, x[n].y);
+                                w4::mma(c[r][n], l2, h2, l3, h3, x[n].z, x[n].w);
                             }
+                        }
                     }
-                    __syncwarp();                  // every lane has read this block
-                    copy(b0 + u + kW4Depth, u, (u + kW4Depth) * (kW4BlockK / 2));
+                    const uint2 sv = w4::lds64(sa + u * L::kSBlock + j * (kW4Rows * 2));
+                    const float s4[4] = {__uint_as_float(sv.x << 16), __uint_as_float(sv.x & 0xFFFF0000u),
+                                         __uint_as_float(sv.y << 16), __uint_as_float(sv.y & 0xFFFF0000u)};
+#pragma unroll
+                    for (int r = 0; r < 2; ++r)
+#pragma unroll
+                        for (int n = 0; n < kNT; ++n) {
+                            acc[r][n][0] = fmaf(s4[2 * r], c[r][n][0], acc[r][n][0]);
+                            acc[r][n][1] = fmaf(s4[2 * r], c[r][n][1], acc[r][n][1]);
+                            acc[r][n][2] = fmaf(s4[2 * r + 1], c[r][n][2], acc[r][n][2]);
+                            acc[r][n][3] = fmaf(s4[2 * r + 1], c[r][n][3], acc[r][n][3]);
+                        }
                 }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) wptr[i] += kW4Depth * (kW4BlockK / 2);
-#pragma unroll
-                for (int n = 0; n < kNT; ++n) xa[n] += kW4Depth * 256;
-                sa += kW4Depth * L::kSBlock;
-                za += kW4Depth * L::kZBlock;
+                __syncwarp();                  // every lane has read this block
+                copy(b0 + u + kW4Depth, u, (u + kW4Depth) * (kW4BlockK / 2));
             }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) wptr[i] += kW4Depth * (kW4BlockK / 2);
+#pragma unroll
+            for (int n = 0; n < kNT; ++n) xa[n] += kW4Depth * 256;
+            sa += kW4Depth * L::kSBlock;
+            za += kW4Depth * L::kZBlock;
         }
-        // This lane's sums of 4 rows for 2 kNT tokens go to the rows' owner: rank
-        // r adds rows 128 r / split .. and keeps [source rank][token][its rows].
-        const int own = kW4Rows / split;            // rows per owner, at least 16
-        const uint32_t slot = red_off + static_cast<uint32_t>(rank * p.tok_cap * own + (r0 & (own - 1))) * 4u;
-        const uint32_t dst = split > 1 ? ptx::map_cluster(slot, static_cast<uint32_t>(r0 / own)) : slot;
-        if (!started) {
-            ptx::cluster_wait_acquire();            // every CTA of the cluster has started
-            started = true;
-        }
+    }
+    // This lane's sums of 4 rows for 2 kNT tokens go to the rows' owner: rank
+    // r adds rows 128 r / split .. and keeps [source rank][token][its rows].
+    const int own = kW4Rows / split;            // rows per owner, at least 16
+    const uint32_t slot = red_off + static_cast<uint32_t>(rank * p.tok_cap * own + (r0 & (own - 1))) * 4u;
+    const uint32_t dst = split > 1 ? ptx::map_cluster(slot, static_cast<uint32_t>(r0 / own)) : slot;
+    if (split > 1) ptx::cluster_wait_acquire();     // every CTA of the cluster has started
 #pragma unroll
-        for (int n = 0; n < kNT; ++n)
+    for (int n = 0; n < kNT; ++n)
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const int tok = 8 * n + 2 * t4 + q;
-                if (tok < ntok)
-                    ptx::st_cluster_v4(dst + static_cast<uint32_t>(tok * own) * 4u, acc[0][n][q], acc[0][n][2 + q],
-                                       acc[1][n][q], acc[1][n][2 + q]);
-            }
-        if (split > 1) ptx::cluster_sync_all();
-        else __syncthreads();
-        const int quads = own / 4;                  // this CTA's runs of 4 rows
-        const float *red = reinterpret_cast<const float *>(smem + (red_off - s_base));
-        for (int i = tid; i < quads * ntok; i += kW4Threads) {
-            const int tok = i / quads, q = i - tok * quads;
-            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int c = 0; c < split; ++c) {
-                const float4 v = *reinterpret_cast<const float4 *>(red + (c * p.tok_cap + tok) * own + 4 * q);
-                sum.x += v.x; sum.y += v.y; sum.z += v.z; sum.w += v.w;
-            }
-            const int row = rank * own + 4 * q;
-            if (row < rows_left) {
-                const __nv_bfloat162 a = __floats2bfloat162_rn(sum.x, sum.y), b = __floats2bfloat162_rn(sum.z, sum.w);
-                uint2 o;
-                o.x = *reinterpret_cast<const uint32_t *>(&a);
-                o.y = *reinterpret_cast<const uint32_t *>(&b);
-                *reinterpret_cast<uint2 *>(p.d + static_cast<size_t>(m0 + tok) * p.N + n0 + row) = o;
-            }
+        for (int q = 0; q < 2; ++q) {
+            const int tok = 8 * n + 2 * t4 + q;
+            if (tok < ntok)
+                ptx::st_cluster_v4(dst + static_cast<uint32_t>(tok * own) * 4u, acc[0][n][q], acc[0][n][2 + q],
+                                   acc[1][n][q], acc[1][n][2 + q]);
         }
-        // with more tokens to come: the sums have been read before anybody stores the next ones
-        if (m0 + kTok < end) {
-            if (split > 1) ptx::cluster_sync_all();
-            else __syncthreads();
+    if (split > 1) ptx::cluster_sync_all();
+    else __syncthreads();
+    const int quads = own / 4;                  // this CTA's runs of 4 rows
+    const float *red = reinterpret_cast<const float *>(smem + (red_off - s_base));
+    for (int i = tid; i < quads * ntok; i += kW4Threads) {
+        const int tok = i / quads, q = i - tok * quads;
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c = 0; c < split; ++c) {
+            const float4 v = *reinterpret_cast<const float4 *>(red + (c * p.tok_cap + tok) * own + 4 * q);
+            sum.x += v.x; sum.y += v.y; sum.z += v.z; sum.w += v.w;
+        }
+        const int row = rank * own + 4 * q;
+        if (row < rows_left) {
+            const __nv_bfloat162 a = __floats2bfloat162_rn(sum.x, sum.y), b = __floats2bfloat162_rn(sum.z, sum.w);
+            uint2 o;
+            o.x = *reinterpret_cast<const uint32_t *>(&a);
+            o.y = *reinterpret_cast<const uint32_t *>(&b);
+            *reinterpret_cast<uint2 *>(p.d + static_cast<size_t>(m0 + tok) * p.N + n0 + row) = o;
         }
     }
 }

@@ -136,6 +136,16 @@ def test_m_grouped(direction, sizes, lead, trail, p, q, ints):
     c.check(c.run(), ints)
 
 
+@pytest.mark.parametrize("ints", [True, False])
+@pytest.mark.parametrize("sizes,lead,trail", [([0, 700, 1, 0, 257, 128, 1300], 3, 300), ([129, 2000, 127], 0, 0)])
+@pytest.mark.parametrize("p,q", [(1032, 1064), (2112, 520), (520, 2112)])
+@pytest.mark.parametrize("direction", [NT, NN])
+def test_m_grouped_on_cta_pairs(direction, sizes, lead, trail, p, q, ints):
+    """256-row tiles with runs that start, end and turn empty inside them."""
+    c = Case(direction, sizes, p, q, lead, trail, ints, seed=len(sizes) + p)
+    c.check(c.run(), ints)
+
+
 K_SIZES = [
     ([1], 0, 0),
     ([0, 15, 16, 17, 0], 2, 5),
