@@ -276,8 +276,9 @@ DG_API dg_status_t dg_m_grouped_bf16_gemm_nt_masked(const void *a, const void *b
  *             DG_ERR_INVALID_VALUE in the device status word; the kernel then
  *             uses them clamped to [0, M_total] and raised to the largest before.
  * Sums are FP32, d is BF16 (RNE).  M_total >= 0; K, N > 0 and multiples of 8;
- * 1 <= G <= 1024.  a and d may be NULL when M_total == 0 (a no-op).  Sizes whose
- * number of 128 x 64 tiles passes 2^31 are DG_ERR_UNSUPPORTED_SHAPE.
+ * 1 <= G <= 1024.  a and d may be NULL when M_total == 0 (a no-op).  M_total above
+ * 2^31 - 1025 and sizes whose number of 32 x 64 tiles passes 2^31 - 1 are
+ * DG_ERR_UNSUPPORTED_SHAPE.
  *
  * Forward:  a [M_total, K], b [G, N, K] (K-major), d [M_total, N]:
  *   D[m,n] = sum_k A[m,k] * B[g(m)][n,k]
@@ -308,7 +309,7 @@ DG_API dg_status_t dg_m_grouped_bf16_gemm_nn_ragged(const void *a, const void *b
  * k_offsets[G]) reach no result, whatever they hold.
  * FP32 results are summed in FP32 with rounding (the tensor core's own sums,
  * which truncate, run over 512 tokens at a time).  M, N > 0 and multiples of 8;
- * 1 <= G <= 1024.  K_total == 0 writes zeros (accumulate: a no-op); a and b may
+ * 1 <= G <= 1024; K_total up to 2^31 - 1025 and G * M * N / 2^14 below 2^31.  K_total == 0 writes zeros (accumulate: a no-op); a and b may
  * then be NULL.  Results do not depend on the order of execution.
  */
 DG_API dg_status_t dg_k_grouped_bf16_gemm_tn_ragged(const void *a, const void *b, void *d,
@@ -328,9 +329,9 @@ DG_API dg_status_t dg_k_grouped_bf16_gemm_tn_ragged(const void *a, const void *b
  *   zeros  [K/group_size, N] uint8, 0..127, or NULL for 8 everywhere
  * q - z is exact and the scale is applied to the group's FP32 sum, so no weight
  * is rounded.  group_size 32, 64 or 128, K % group_size == 0, N % 8 == 0,
- * N <= 65535 * 128.  Rows are taken up to 32 at a time and the weights
- * read once for each such run, so the call is meant for few (M <= 65535 * 32).  M == 0 is a no-op
- * (x and d may be NULL).
+ * N <= 65535 * 128.  Rows are taken 8, 16 or 32 at a time and the weights read
+ * once for each such run, so the call is meant for few; M <= 2000000.  M == 0 is
+ * a no-op (x and d may be NULL).
  */
 DG_API dg_status_t dg_w4_gemv_nt(const void *x, const uint8_t *w, const void *scales,
                                  const uint8_t *zeros, void *d, int M, int N, int K, int group_size,

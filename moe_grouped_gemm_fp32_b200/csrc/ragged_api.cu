@@ -24,6 +24,7 @@ dg_status_t check_ragged(const void *a, const void *b, const void *d, const int3
     if (rows < 0 || p <= 0 || q <= 0 || G <= 0) return DG_ERR_INVALID_VALUE;
     if (p % 8 != 0 || q % 8 != 0) return DG_ERR_UNSUPPORTED_SHAPE;        // 16-byte rows
     if (G > dg::kMaxGroups || p > (1 << 30) || q > (1 << 30)) return DG_ERR_UNSUPPORTED_SHAPE;
+    if (rows > kMaxInt - 1024) return DG_ERR_UNSUPPORTED_SHAPE;           // a tile's rows past the end stay 32-bit
     if (!aligned16(a) || !aligned16(b) || !aligned16(d)) return DG_ERR_MISALIGNED;
     return DG_SUCCESS;
 }

@@ -14,12 +14,15 @@
 namespace {
 using namespace dg_host;
 
+constexpr int kMaxRows = 2000000;   // their runs of 32, and one more for each expert, are grid.z (65535 at most)
+
 dg_status_t check_w4(const void *x, const void *w, const void *s, const void *z, const void *d, int M, int N, int K,
                      int G, int group_size) {
     if (!w || !s || (M > 0 && (!x || !d))) return DG_ERR_INVALID_VALUE;
     if (M < 0 || N <= 0 || K <= 0 || G <= 0) return DG_ERR_INVALID_VALUE;
     if (group_size != 32 && group_size != 64 && group_size != 128) return DG_ERR_UNSUPPORTED_SHAPE;
     if (K % group_size != 0 || N % 8 != 0 || G > 1024) return DG_ERR_UNSUPPORTED_SHAPE;
+    if (M > kMaxRows) return DG_ERR_UNSUPPORTED_SHAPE;
     if (K > (1 << 30) || (N + dg::kW4Rows - 1) / dg::kW4Rows > 65535) return DG_ERR_UNSUPPORTED_SHAPE;   // grid.y
     if (!aligned16(x) || !aligned16(w) || !aligned16(s) || !aligned16(z) || !aligned16(d)) return DG_ERR_MISALIGNED;
     return DG_SUCCESS;
@@ -28,7 +31,6 @@ dg_status_t check_w4(const void *x, const void *w, const void *s, const void *z,
 template <int kGs, int kNT, bool kZeros>
 dg_status_t launch_w4(dg::W4Params p, int split, int runs, cudaStream_t stream) {
     using L = dg::W4Smem<kGs>;
-    if (runs > 65535) return DG_ERR_UNSUPPORTED_SHAPE;      // grid.z
     auto kernel = dg::w4_gemv_kernel<kGs, kNT, kZeros>;
     const int blocks = (p.K + dg::kW4BlockK - 1) / dg::kW4BlockK;
     const int per_cta = (blocks + split - 1) / split;

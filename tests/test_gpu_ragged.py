@@ -340,7 +340,7 @@ def test_a_layer_trains_as_in_64_bits():
     dx = torch.zeros(tokens, H, device="cuda").index_add(0, src, dx.float())
     # at most six BF16 roundings of 2^-8 lie between the inputs and any of these
     for name, g, e in (("out", got, out), ("dw2", dw2, W2.grad), ("dw1", dw1, W1.grad), ("dx", dx, X.grad)):
-        rel = float((g.double() - e).norm() / e.norm())
+        rel = float((g.double() - e.detach()).norm() / e.detach().norm())
         assert rel <= 6 * 2.0 ** -8, (name, rel)
 
 

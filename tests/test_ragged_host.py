@@ -43,6 +43,7 @@ def test_m_grouped_refusals(L, name):
     assert _call(f, RAGGED, N=252) == 3
     assert _call(f, RAGGED, K=516) == 3
     assert _call(f, RAGGED, M=(1 << 31) - 1, N=1 << 20) == 3      # more than 2^31 tiles
+    assert _call(f, RAGGED, M=(1 << 31) - 1) == 3                 # a tile's last rows would pass 32 bits
     if not torch.cuda.is_available():
         assert _call(f, RAGGED) == OK_BUT_NO_DEVICE
 
@@ -63,6 +64,7 @@ def test_k_grouped_refusals(L):
     assert _call(f, WGRAD, M=260) == 3
     assert _call(f, WGRAD, N=130) == 3
     assert _call(f, WGRAD, G=1024, M=1 << 20, N=1 << 20) == 3
+    assert _call(f, WGRAD, K=(1 << 31) - 1) == 3
     if not torch.cuda.is_available():
         assert _call(f, WGRAD) == OK_BUT_NO_DEVICE
 
@@ -85,6 +87,7 @@ def test_w4_refusals(L):
         assert _call(f, base, gs=0) == 3
         assert _call(f, base, K=480, gs=64) == 3
         assert _call(f, base, N=65536 * 128) == 3
+        assert _call(f, base, M=2000001) == 3
         if not torch.cuda.is_available():
             assert _call(f, base) == OK_BUT_NO_DEVICE
     assert _call(L.dg_m_grouped_w4_gemv_nt_ragged, W4G, off=None) == 1
