@@ -133,64 +133,84 @@ __host__ __device__ constexpr uint32_t ragged_idesc(int m, int n, bool a_mn, boo
            (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
 }
 
+// The tiles of the experts in order, and where the walk stands: every role goes
+// through its CTA's tiles (t ascending) by itself.  What holds for an expert is kept
+// while its tiles last, and divisions are by a reciprocal: the walk is one thread's
+// chain of dependent instructions once a tile, which bounds tiles with few K-blocks.
+template <int kDir, int kBN, int kCtaGroup, int kCtaRows>
 struct RaggedTile {
-    int g = 0;     // in: where the search begins
+    static constexpr int kRows = kCtaRows * kCtaGroup;
+    // the tile
+    int g;
     int row0;      // kNT, kNN: first token row of the tile (in the buffer); kTN: first output row
     int row_end;   // exclusive bound of its valid rows
     int n0;
     int num_kb;    // K-blocks of 64
     int tail;      // kTN: tokens in the last K-block (1..64), 64 elsewhere
-};
-
-template <int kDir, int kBN, int kCtaGroup, int kCtaRows>
-struct RaggedMap {
-    static constexpr int kRows = kCtaRows * kCtaGroup;
+    int tok0;      // first token of the expert
+    // the expert
+    int base, next;        // its tiles [base, next)
+    unsigned rb, height;   // row blocks, and those of a band
+    float inv;             // 1 / height
 
     __device__ static int row_blocks(const RaggedParams &p, const int *offs, int g) {
         const int rows = kDir == kTN ? p.M : offs[g + 1] - offs[g];
         return (rows + kRows - 1) / kRows;
     }
-    // n / d by a reciprocal, put right by a step (small n; the division's latency is in
-    // every role's way once a tile)
-    __device__ static unsigned quotient(unsigned n, unsigned d) {
+    // n / d with inv = 1 / d, put right by a step (small n)
+    __device__ static unsigned quotient(unsigned n, unsigned d, float inv) {
         if (n >= (1u << 22)) return n / d;
-        unsigned q = static_cast<unsigned>(__fdividef(static_cast<float>(n), static_cast<float>(d)));
+        unsigned q = static_cast<unsigned>(static_cast<float>(n) * inv);
         if (q * d > n) --q;
         if (n - q * d >= d) ++q;
         return q;
     }
-    __device__ static int count(const RaggedParams &p, const int *prefix) { return prefix[p.G]; }
 
-    __device__ static void decode(int t, const RaggedParams &p, const int *offs, const int *prefix,
-                                  RaggedTile &tl) {
-        while (prefix[tl.g + 1] <= t) ++tl.g;          // tiles come in order: on from the last one's expert
-        const int g = tl.g;
-        const unsigned local = t - prefix[g];
+    __device__ __forceinline__ RaggedTile() : g(-1), base(0), next(0) {}
+
+    __device__ __forceinline__ void decode(int t, const RaggedParams &p, const int *offs, const int *prefix) {
         const unsigned nb = (p.N + kBN - 1) / kBN;
-        const unsigned rb = row_blocks(p, offs, g);
-        unsigned height = rb, band = 0;
+        if (t >= next) {
+            do {
+                ++g;
+                base = next;
+                if (kDir == kTN) next += row_blocks(p, offs, 0) * static_cast<int>(nb);    // alike for all
+                else next = prefix[g + 1];
+            } while (t >= next);
+            tok0 = offs[g];
+            const int end = offs[g + 1];
+            rb = row_blocks(p, offs, g);
+            height = rb;
+            if (rb > kRaggedBand) {
+                const unsigned bands = (rb + kRaggedBand - 1) / kRaggedBand;
+                height = (rb + bands - 1) / bands;
+            }
+            inv = __fdividef(1.f, static_cast<float>(height));
+            if (kDir == kTN) {
+                row_end = p.M;
+                num_kb = (end - tok0 + kRaggedBlockK - 1) / kRaggedBlockK;
+                tail = end - tok0 - (num_kb - 1) * kRaggedBlockK;
+            } else {
+                row_end = end;
+                num_kb = (p.K + kRaggedBlockK - 1) / kRaggedBlockK;
+                tail = kRaggedBlockK;
+            }
+        }
+        unsigned in_band = t - base, first = 0, width = height;
+        float inv_w = inv;
         if (rb > kRaggedBand) {
-            const unsigned bands = (rb + kRaggedBand - 1) / kRaggedBand;
-            height = quotient(rb + bands - 1, bands);
-            band = quotient(local, height * nb);
+            const unsigned band = in_band / (height * nb);
+            first = band * height;
+            in_band -= first * nb;
+            if (rb - first < height) {
+                width = rb - first;
+                inv_w = __fdividef(1.f, static_cast<float>(width));
+            }
         }
-        const unsigned width = min(height, rb - band * height);
-        const unsigned in_band = local - band * height * nb;
-        const unsigned col = quotient(in_band, width);
-        const int row = static_cast<int>(band * height + in_band - col * width) * kRows;
-        tl.n0 = static_cast<int>(col) * kBN;
-        const int tokens = offs[g + 1] - offs[g];
-        if (kDir == kTN) {
-            tl.row0 = row;
-            tl.row_end = p.M;
-            tl.num_kb = (tokens + kRaggedBlockK - 1) / kRaggedBlockK;
-            tl.tail = tokens - (tl.num_kb - 1) * kRaggedBlockK;
-        } else {
-            tl.row0 = offs[g] + row;
-            tl.row_end = offs[g + 1];
-            tl.num_kb = (p.K + kRaggedBlockK - 1) / kRaggedBlockK;
-            tl.tail = kRaggedBlockK;
-        }
+        const unsigned col = quotient(in_band, width, inv_w);
+        const int row = static_cast<int>(first + in_band - col * width) * kRows;
+        n0 = static_cast<int>(col) * kBN;
+        row0 = kDir == kTN ? row : tok0 + row;
     }
 };
 
@@ -213,62 +233,87 @@ __device__ __forceinline__ void add8(__nv_bfloat16 *d, const float *v) {
     *o = make_uint4(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]), pack_bf16x2(s[4], s[5]), pack_bf16x2(s[6], s[7]));
 }
 
-// 32 columns of this lane's row into a warp's box of 32 rows, its 16-byte pieces
-// permuted by the row against bank conflicts ...
+// A warp's way from accumulator rows (one a lane) to runs of a row in memory, 32
+// columns at a time: `put` writes a box of 32 rows to shared memory, its 16-byte
+// pieces permuted by the row against bank conflicts, and stores it in runs of 64 (BF16)
+// or 128 bytes of a row.  Addresses that do not change are kept: the epilogue's
+// instructions are what bounds tiles with few products.
 template <bool kF32>
-__device__ __forceinline__ void stage32(uint8_t *box, int lane, const float *v) {
-    if constexpr (kF32) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            *reinterpret_cast<float4 *>(box + lane * 128 + ((j ^ (lane & 7)) << 4)) =
-                make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<uint4 *>(box + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
-                make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
-                           pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
-    }
-}
+struct BoxWriter {
+    static constexpr int kElem = kF32 ? 4 : 2;
+    static constexpr int kPieces = kF32 ? 8 : 4;        // 16-byte pieces of a row
+    static constexpr int kRowsAt = 32 / kPieces;        // rows of one store instruction
+    uint32_t in[kPieces], out[kPieces];                 // this lane's pieces in shared memory
+    uint8_t *dst[kPieces];                              // and in memory, for the tile's first columns
+    uint32_t row_ok;                                    // a bit for each of them
+    int col;                                            // its first column in a box
 
-// ... and from there to memory, runs of 64 (BF16) or 128 bytes of a row: `rows` of
-// them exist, of `cols` columns (a multiple of 8).  d: this lane's 16 bytes of the
-// first row that it stores (unstage_row, unstage_col), step: between its rows.
-template <bool kF32>
-__device__ __forceinline__ int unstage_row(int lane) { return kF32 ? lane / 8 : lane / 4; }
-template <bool kF32>
-__device__ __forceinline__ int unstage_col(int lane) { return kF32 ? lane % 8 * 4 : lane % 4 * 8; }
-template <bool kF32>
-__device__ __forceinline__ void unstage32(const uint8_t *box, int lane, uint8_t *d, size_t step, int rows, int cols, bool add) {
-    constexpr int kPieces = kF32 ? 8 : 4;               // 16-byte pieces of a row
-    constexpr int kRowsAt = 32 / kPieces;
-    const int r0 = unstage_row<kF32>(lane), piece = lane % kPieces;
-    uint4 v[kPieces];
+    __device__ __forceinline__ BoxWriter(uint32_t box, int lane) {
+        col = lane % kPieces * (16 / kElem);
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-        const int r = r0 + i * kRowsAt;
-        v[i] = *reinterpret_cast<const uint4 *>(box + (kF32 ? r * 128 + ((piece ^ (r & 7)) << 4)
-                                                            : r * 64 + ((piece ^ ((r >> 1) & 3)) << 4)));
+        for (int i = 0; i < kPieces; ++i) {
+            const int r = lane / kPieces + i * kRowsAt;
+            in[i] = box + lane * (32 * kElem) + ((i ^ swizzle(lane)) << 4);
+            out[i] = box + r * (32 * kElem) + ((lane % kPieces ^ swizzle(r)) << 4);
+        }
     }
-    if (unstage_col<kF32>(lane) >= cols) return;
+    __device__ __forceinline__ static int swizzle(int row) { return kF32 ? row & 7 : (row >> 1) & 3; }
+
+    // base: the warp's first row and the tile's first column; ld: bytes between rows;
+    // rows: how many of the 32 exist
+    __device__ __forceinline__ void tile(uint8_t *base, size_t ld, int rows, int lane) {
+        row_ok = 0;
+        uint8_t *d = base + static_cast<size_t>(lane / kPieces) * ld + col * kElem;
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-        if (r0 + i * kRowsAt < rows) {
-            if constexpr (kF32) {
-                float4 f = make_float4(__uint_as_float(v[i].x), __uint_as_float(v[i].y), __uint_as_float(v[i].z),
-                                       __uint_as_float(v[i].w));
-                if (add) {
-                    const float4 x = *reinterpret_cast<const float4 *>(d);
-                    f.x += x.x; f.y += x.y; f.z += x.z; f.w += x.w;
+        for (int i = 0; i < kPieces; ++i) {
+            dst[i] = d;
+            d += kRowsAt * ld;
+            if (lane / kPieces + i * kRowsAt < rows) row_ok |= 1u << i;
+        }
+    }
+
+    // v: 32 columns of this lane's row, from column `c` of the tile's first; `cols` of
+    // them exist (a multiple of 8)
+    __device__ __forceinline__ void put(int c, const float *v, int cols, bool add) const {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            uint4 x;
+            if constexpr (kF32)
+                x = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
+                               __float_as_uint(v[4 * i + 3]));
+            else
+                x = make_uint4(pack_bf16x2(v[8 * i], v[8 * i + 1]), pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
+                               pack_bf16x2(v[8 * i + 4], v[8 * i + 5]), pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(in[i]), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w)
+                         : "memory");
+        }
+        __syncwarp();
+        uint4 x[kPieces];
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i)
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(x[i].x), "=r"(x[i].y), "=r"(x[i].z), "=r"(x[i].w)
+                         : "r"(out[i])
+                         : "memory");
+        if (col < cols) {
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+                if ((row_ok >> i) & 1u) {
+                    uint4 *o = reinterpret_cast<uint4 *>(dst[i] + c * kElem);
+                    if (kF32 && add) {
+                        const float4 y = *reinterpret_cast<const float4 *>(o);
+                        x[i].x = __float_as_uint(__uint_as_float(x[i].x) + y.x);
+                        x[i].y = __float_as_uint(__uint_as_float(x[i].y) + y.y);
+                        x[i].z = __float_as_uint(__uint_as_float(x[i].z) + y.z);
+                        x[i].w = __float_as_uint(__uint_as_float(x[i].w) + y.w);
+                    }
+                    *o = x[i];
                 }
-                *reinterpret_cast<float4 *>(d) = f;
-            } else {
-                *reinterpret_cast<uint4 *>(d) = v[i];
             }
         }
-        d += step;
+        __syncwarp();
     }
-}
+};
 
 // tm_a, tm_b: see the operand table above (kNT, kNN single-CTA: A boxes of 32 rows).
 // tm_d: boxes of 32 columns by 32 rows of D [groups][rows][N] (kTN: one group per expert).
@@ -278,7 +323,7 @@ __global__ void __launch_bounds__(ragged_threads(kF32), 1)
 ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                    const RaggedParams p) {
     using L = RaggedSmem<kDir, kBN, kStages, kCtaGroup, kF32, kRows>;
-    using TM = RaggedMap<kDir, kBN, kCtaGroup, kRows>;
+    using Tile = RaggedTile<kDir, kBN, kCtaGroup, kRows>;
     static_assert(!kF32 || kDir == kTN, "FP32 output: weight gradient");
     static_assert(kRows == kTileX || (kRows == 32 && kDir != kTN && kCtaGroup == 1), "thin tiles: one CTA, K-major A");
     // a thin tile's A descriptor runs on over 96 rows' bytes that follow its 32
@@ -372,7 +417,7 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
         int carry = 0;
         for (int base = 0; base < p.G; base += 32) {
             const int g = base + lane;
-            const int tiles = g < p.G ? TM::row_blocks(p, offs, g) * nb : 0;
+            const int tiles = g < p.G ? Tile::row_blocks(p, offs, g) * nb : 0;
             int incl = tiles;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -399,7 +444,7 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
     ptx::tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
 
-    const int num_tiles = TM::count(p, prefix);
+    const int num_tiles = prefix[p.G];
     const int t_first = static_cast<int>(blockIdx.x) / kCtaGroup;
     const int t_step = static_cast<int>(gridDim.x) / kCtaGroup;
 
@@ -412,9 +457,9 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
                 uint32_t phase = 0, tail_phase = 0, tail_armed = 0;   // a bit per stage
                 long long issued = 0;
                 bool ok = (p.debug_flags & kDebugProducerIdle) == 0;
-                RaggedTile tl;
+                Tile tl;
                 for (int t = t_first; ok && t < num_tiles; t += t_step) {
-                    TM::decode(t, p, offs, prefix, tl);
+                    tl.decode(t, p, offs, prefix);
                     // kNT, kNN: rows of A that this CTA loads, in boxes of 32 (single CTAs) or 128
                     const int a_boxes = (kDir != kTN && !kPair) ? (min(tl.row_end - tl.row0, kRows) + 31) / 32 : 0;
                     const uint32_t bytes = (kDir != kTN && !kPair) ? L::kSub * (a_boxes * 4096u + L::kBBytes)
@@ -446,7 +491,7 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
                             else ptx::tma_load_3d(dst, m, bar, c0, c1, c2);
                         };
                         if constexpr (kDir == kTN) {
-                            const int tok = offs[tl.g] + k0;
+                            const int tok = tl.tok0 + k0;
                             for (int i = 0; i < 2; ++i)
                                 load(sa + i * 8192u, &tm_a, tl.row0 + pair_rank * kTileX + 64 * i, tok, 0);
                             for (int i = 0; i < L::kBCols / 64; ++i)
@@ -504,9 +549,9 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
                 const uint32_t idesc = ragged_idesc(kTileX * kCtaGroup, kBN, kAMn, kBMn);
                 constexpr uint32_t kStepA = kAMn ? 2048 >> 4 : 32 >> 4;   // 16 reduced indices
                 constexpr uint32_t kStepB = kBMn ? 2048 >> 4 : 32 >> 4;
-                RaggedTile tl;
+                Tile tl;
                 for (int t = t_first; ok && t < num_tiles; t += t_step) {
-                    TM::decode(t, p, offs, prefix, tl);
+                    tl.decode(t, p, offs, prefix);
                     // one accumulator for the tile (nothing in it for an expert without tokens), or
                     // one for each segment
                     const int seg = kPromote ? kSegBlocks : max(tl.num_kb, 1);
@@ -553,9 +598,9 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
             // ======================================================== clears ragged token rows
             long long block = 0;                  // K-blocks of the tiles before
             uint32_t tail_phase = 0;              // a bit per stage
-            RaggedTile tl;
+            Tile tl;
             for (int t = t_first; t < num_tiles; t += t_step) {
-                TM::decode(t, p, offs, prefix, tl);
+                tl.decode(t, p, offs, prefix);
                 block += tl.num_kb;
                 if (tl.num_kb == 0 || (tl.tail & 15) == 0) continue;
                 const int stage = static_cast<int>((block - 1) % kStages);
@@ -589,9 +634,8 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
         const int half = ((warp - kEpiWarp0) >> 2) & 1;
         const int group = (warp - kEpiWarp0) >> 3;          // of the accumulators' rotation (FP32: one group for both)
         const int wrow = pair_rank * kTileX + quarter * 32;  // the warp's first row in a tile
-        uint8_t *out = smem + L::kOutOffset + (warp - kEpiWarp0) * L::kBoxBytes;
+        BoxWriter<kF32> writer(s_base + L::kOutOffset + (warp - kEpiWarp0) * L::kBoxBytes, lane);
         constexpr int kElem = kF32 ? 4 : 2;
-        const size_t step = static_cast<size_t>(p.N) * kElem * (kF32 ? 4 : 8);   // between a lane's stored rows
         const bool add = kDir == kTN && p.accumulate;
         int buf = group;
         uint32_t tphase = 0;
@@ -607,15 +651,14 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
             if (kPromote) buf ^= 1;
             if (!kPromote || buf == 0) tphase ^= 1u;
         };
-        RaggedTile tl;
+        Tile tl;
         const int e_step = kPromote ? t_step : 2 * t_step;
         for (int t = t_first + group * t_step; ok && t < num_tiles; t += e_step) {
-            TM::decode(t, p, offs, prefix, tl);
+            tl.decode(t, p, offs, prefix);
             const int rows = min(tl.row_end, tl.row0 + pair_rank * kTileX + kRows) - (tl.row0 + wrow);   // of the warp's 32
             const int c0 = tl.n0 + half * kHalf;
             const size_t row0 = (kDir == kTN ? static_cast<size_t>(tl.g) * p.M : 0) + tl.row0 + wrow;
-            uint8_t *dst = static_cast<uint8_t *>(p.d) +
-                           ((row0 + unstage_row<kF32>(lane)) * p.N + c0 + unstage_col<kF32>(lane)) * kElem;
+            writer.tile(static_cast<uint8_t *>(p.d) + (row0 * p.N + c0) * kElem, static_cast<size_t>(p.N) * kElem, rows, lane);
             auto put = [&](int c, const float *v) {      // columns c0 + c .. + 31 of this lane's row
                 if (c0 + c >= p.N || rows <= 0) return;
                 if (kDir == kTN && !kF32 && add) {       // BF16 is added in FP32: before it is rounded
@@ -626,10 +669,7 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
                                 add8(static_cast<__nv_bfloat16 *>(p.d) + (row0 + lane) * p.N + c0 + c + j, v + j);
                     return;
                 }
-                stage32<kF32>(out, lane, v);
-                __syncwarp();
-                unstage32<kF32>(out, lane, dst + c * kElem, step, rows, p.N - c0 - c, add);
-                __syncwarp();
+                writer.put(c, v, p.N - c0 - c, add);
             };
             if constexpr (kPromote) {
                 float acc[kHalf];
@@ -663,7 +703,7 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
                 const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
                                        static_cast<uint32_t>(buf * kBN + half * kHalf);
                 if (tl.num_kb > 0 || !add) {
-#pragma unroll 1
+#pragma unroll
                     for (int c = 0; c < kHalf; c += 32) {
                         float v[32];
                         if (kDir != kTN || tl.num_kb > 0) {
