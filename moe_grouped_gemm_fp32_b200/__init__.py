@@ -125,6 +125,16 @@ def _th():
     return _torch
 
 
+_one_gpu = None
+
+
+def _single_gpu() -> bool:
+    global _one_gpu
+    if _one_gpu is None:
+        _one_gpu = _th().cuda.device_count() == 1
+    return _one_gpu
+
+
 def _stream_handle(stream) -> Optional[int]:
     if stream is None:
         c = _th()._C
@@ -177,6 +187,10 @@ def _call(where, fn, tensors, stream, *args):
     """Call ``fn(*args, stream_handle)`` and raise on a non-success status.
     The C library launches on the current CUDA device, so every tensor (and
     the stream, if given) must live on that device."""
+    if getattr(tensors[0], "is_cuda", False) and _single_gpu():
+        # every CUDA tensor and stream is on it
+        _check(fn(*args, _stream_handle(stream)), where)
+        return
     dev = tensors[0].device
     for t in tensors:
         if t.device != dev:

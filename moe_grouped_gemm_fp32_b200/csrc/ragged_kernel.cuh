@@ -307,7 +307,8 @@ struct BoxWriter {
                         x[i].z = __float_as_uint(__uint_as_float(x[i].z) + y.z);
                         x[i].w = __float_as_uint(__uint_as_float(x[i].w) + y.w);
                     }
-                    *o = x[i];
+                    if constexpr (kF32) __stcs(o, x[i]);        // large, and not read soon: 118 -> 114 us for 64 experts
+                    else *o = x[i];
                 }
             }
         }
