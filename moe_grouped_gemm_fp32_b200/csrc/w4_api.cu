@@ -35,15 +35,14 @@ dg_status_t launch_w4(dg::W4Params p, int split, int runs, cudaStream_t stream) 
     const int blocks = (p.K + dg::kW4BlockK - 1) / dg::kW4BlockK;
     const int per_cta = (blocks + split - 1) / split;
     p.tok_cap = p.M < 8 * kNT ? p.M : 8 * kNT;
-    p.chunk = per_cta;
-    if (p.chunk > dg::w4_max_chunk<kNT>()) p.chunk = dg::w4_max_chunk<kNT>();
-    const int smem = L::bytes(p.tok_cap, p.chunk, kZeros);
+    p.bufs = per_cta > dg::kW4Chunk ? 2 : 1;
+    const int smem = L::bytes(p.tok_cap, p.bufs, kZeros);
     // one-time per-device set-up (idempotent; the atomic flag keeps racing first calls defined)
     static std::atomic<bool> configured[kMaxDevices] = {};
     int dev = 0;
     cudaGetDevice(&dev);
     if (!configured[dev].load(std::memory_order_acquire)) {
-        const int most = L::bytes(8 * kNT, dg::w4_max_chunk<kNT>(), kZeros);
+        const int most = L::bytes(8 * kNT, 2, kZeros);
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
         if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(w4 smem)");
         configured[dev].store(true, std::memory_order_release);
@@ -61,8 +60,8 @@ dg_status_t launch_w4(dg::W4Params p, int split, int runs, cudaStream_t stream) 
     cfg.attrs = attr;
     cfg.numAttrs = split > 1 ? 1 : 0;
     if (verbose())
-        std::fprintf(stderr, "[dg] w4_gemv group=%d tokens=%d split=%d grid=%ux%ux%u chunk=%d smem=%d\n", kGs, 8 * kNT,
-                     split, cfg.gridDim.x, cfg.gridDim.y, cfg.gridDim.z, p.chunk, smem);
+        std::fprintf(stderr, "[dg] w4_gemv group=%d tokens=%d split=%d grid=%ux%ux%u bufs=%d smem=%d\n", kGs, 8 * kNT,
+                     split, cfg.gridDim.x, cfg.gridDim.y, cfg.gridDim.z, p.bufs, smem);
     cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
     return e == cudaSuccess ? DG_SUCCESS : cuda_fail(e, "w4_gemv_kernel launch");
 }

@@ -10,9 +10,12 @@
 // read once); what stands in the way is the number of instructions that unpack
 // them: at the memory's rate an SM has 2.8 lane instructions for each weight.
 //   * A CTA owns 128 weight rows and a range of K, each of its 4 warps 32 rows.
-//     A warp copies its own rows asynchronously, kDepth blocks of 128 k ahead, and
-//     waits for nobody; x, permuted once to the order in which the products want
-//     it, and the scales are staged by the whole CTA.
+//     A warp copies its own rows asynchronously, two blocks of 128 k ahead, and
+//     waits for nobody; x and the scales come in chunks of 4 blocks, copied by the
+//     whole CTA a chunk ahead (staged when its turn came, a chunk held up all warps for
+//     a trip to L2: one token, 4096 x 7168, 8.8 us against 7.8).  x is paired for the
+//     products once, on its way between two places in shared memory: paired after each
+//     read it costs 16 more instructions a block, and 16384 x 7168 took 24.5 us, not 19.3.
 //   * A cluster of `split` CTAs shares the 128 rows along K where there are too
 //     few row blocks to fill the GPU; each CTA stores its FP32 partial sums into
 //     the shared memory of the rows' owners, which add them in rank order.
@@ -47,7 +50,6 @@ constexpr int kW4Rows = 128;            // weight rows per CTA
 constexpr int kW4BlockK = 128;          // k per block: 16 bytes of a row for each lane of a quad
 constexpr int kW4Depth = 2;             // blocks in flight per warp, a power of two
 constexpr int kW4WarpBlock = 32 * (kW4BlockK / 2);                  // bytes of a warp's rows in a block
-constexpr int kW4RedPitch = kW4Rows;
 constexpr unsigned kW4SiteBadOffsets = 14;
 
 struct W4Params {
@@ -60,30 +62,27 @@ struct W4Params {
     unsigned *status;
     int M, N, K, G;
     int tok_cap;                // tokens that shared memory holds: min(8 kNT, M)
-    int chunk;                  // K blocks that it holds
+    int bufs;                   // chunks of scales that it holds: 2, or 1 where a CTA has no more
 };
 
-// K blocks of x and scales staged at once, at most; a multiple of kW4Depth, small
-// enough for five CTAs on an SM (kNT 1; four and three for 2 and 4)
-template <int kNT>
-constexpr int w4_max_chunk() { return kNT == 1 ? 8 : 4; }
+// x and scales arrive in chunks of 4 blocks, the next one while this one is used.
+constexpr int kW4Chunk = 4;
+constexpr int kW4XPitch = kW4Chunk * kW4BlockK * 2 + 64;       // bytes; 8 rows' reads are free of bank conflicts
 
-__host__ __device__ constexpr int w4_x_pitch(int chunk) { return chunk * kW4BlockK * 2 + 64; }   // bytes
-
-// Byte offsets: the warps' weight blocks, x (one row more than tokens: zeros), scales, zero points, partial sums.
+// Byte offsets: the warps' weight blocks, x paired (and a row of zeros), x as it
+// arrives, scales, zero points, partial sums.
 template <int kGs>
 struct W4Smem {
     static constexpr int kSBlock = kW4BlockK / kGs * kW4Rows * 2;   // scales of a block
     static constexpr int kZBlock = kW4BlockK / kGs * kW4Rows;
     static constexpr int kXOffset = kW4Threads / 32 * kW4Depth * kW4WarpBlock;
-    __host__ __device__ static int s_offset(int tok_cap, int chunk) { return kXOffset + (tok_cap + 1) * w4_x_pitch(chunk); }
-    __host__ __device__ static int z_offset(int tok_cap, int chunk) { return s_offset(tok_cap, chunk) + chunk * kSBlock; }
-    __host__ __device__ static int red_offset(int tok_cap, int chunk, bool zeros) {
-        return z_offset(tok_cap, chunk) + (zeros ? chunk * kZBlock : 0);
+    __host__ __device__ static int raw_offset(int tok_cap) { return kXOffset + (tok_cap + 1) * kW4XPitch; }
+    __host__ __device__ static int s_offset(int tok_cap) { return raw_offset(tok_cap) + tok_cap * kW4Chunk * kW4BlockK * 2; }
+    __host__ __device__ static int z_offset(int tok_cap, int bufs) { return s_offset(tok_cap) + bufs * kW4Chunk * kSBlock; }
+    __host__ __device__ static int red_offset(int tok_cap, int bufs, bool zeros) {
+        return z_offset(tok_cap, bufs) + (zeros ? bufs * kW4Chunk * kZBlock : 0);
     }
-    static int bytes(int tok_cap, int chunk, bool zeros) {
-        return red_offset(tok_cap, chunk, zeros) + tok_cap * kW4RedPitch * 4;
-    }
+    static int bytes(int tok_cap, int bufs, bool zeros) { return red_offset(tok_cap, bufs, zeros) + tok_cap * kW4Rows * 4; }
 };
 
 namespace w4 {
@@ -246,6 +245,7 @@ w4_gemv_kernel(const W4Params p) {
     constexpr int kTok = 8 * kNT;
     constexpr int kGroups = kW4BlockK / kGs;        // scale groups of a block
     constexpr int kWords = 4 / kGroups;             // words of a lane in a group
+    constexpr int kRawTok = kW4Chunk * kW4BlockK * 2;   // bytes of a token's x in a chunk
     extern __shared__ __align__(128) uint8_t smem[];   // the reads' permutation wants 64
     const uint32_t s_base = ptx::smem_u32(smem);
     const int tid = threadIdx.x;
@@ -274,24 +274,23 @@ w4_gemv_kernel(const W4Params p) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         wrow[i] = p.w + (e * p.N + n0 + min(r0 + i, rows_left - 1)) * static_cast<size_t>(p.K / 2) + t4 * 16;
-    const uint32_t x_pitch = w4_x_pitch(p.chunk);
-    const uint32_t s_off = s_base + L::s_offset(p.tok_cap, p.chunk) + r0 * 2;
-    const uint32_t z_off = s_base + L::z_offset(p.tok_cap, p.chunk) + r0;
+    const uint32_t s_off = s_base + L::s_offset(p.tok_cap) + r0 * 2;
+    const uint32_t z_off = s_base + L::z_offset(p.tok_cap, p.bufs) + r0;
 
     // first of this lane's reads of a row: a 16-byte piece, 8 bytes or a word of one
     const uint32_t w_read = s_base + warp * (kW4Depth * kW4WarpBlock) +
                             (kGs == 128 ? w4::w_at(0, g8, t4)
                              : kGs == 64 ? w4::w_at(0, g8, t4 >> 1) + (t4 & 1) * 8 : w4::w_at(0, g8, 0) + t4 * 4);
     const uint32_t w_off = s_base + warp * (kW4Depth * kW4WarpBlock);
-    const uint32_t red_off = s_base + L::red_offset(p.tok_cap, p.chunk, kZeros);
-    const uint32_t zero_row = s_base + L::kXOffset + p.tok_cap * x_pitch;
+    const uint32_t red_off = s_base + L::red_offset(p.tok_cap, p.bufs, kZeros);
+    const uint32_t zero_row = s_base + L::kXOffset + p.tok_cap * kW4XPitch;
     uint32_t bias;
     asm volatile("mov.u32 %0, 0x43004300;" : "=r"(bias));
-    for (int i = tid * 16; i < static_cast<int>(x_pitch); i += kW4Threads * 16)
+    for (int i = tid * 16; i < kW4XPitch; i += kW4Threads * 16)
         w4::sts128(zero_row + i, make_uint4(0u, 0u, 0u, 0u));
     if (split > 1) ptx::cluster_arrive_relaxed();   // waited for before the first store into another CTA
 
-    // A warp's rows of block `blk`, whose slot `u` is blk - blk0 modulo kW4Depth, from
+    // A warp's rows of block `blk`, whose slot `u` is its place in its chunk modulo kW4Depth, from
     // `ahead` bytes past wptr; zeros past K.
     const uint8_t *wptr[4];
     const int full = min(blk1, p.K / kW4BlockK);
@@ -317,132 +316,154 @@ w4_gemv_kernel(const W4Params p) {
         for (int i = 0; i < kNT; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[r][i][j] = 0.f;
-    // where this lane's rows of x lie: tokens past the expert's read zeros
-    uint32_t xrow[kNT];
+    const uint32_t raw = s_base + L::raw_offset(p.tok_cap) + (tid >> 4) * kRawTok + (tid & 15) * 16;
+    // x of the blocks c .. c + 3 as it is, their scales into buffer `buf`
+    auto stage = [&](int c, int buf) {
+        const int nblk = min(kW4Chunk, blk1 - c);
+        // x in pieces of 8 values; zeros past K.  Thread: piece tid % 16 of a block, tokens
+        // tid / 16, tid / 16 + 8, ..., which it alone reads again (pair).
+        const int left = p.K - (c * kW4BlockK + (tid & 15) * 8);
+#pragma unroll
+        for (int n = 0; n < kNT; ++n) {
+            const int tok = 8 * n + (tid >> 4);
+            if (tok < ntok) {
+                const __nv_bfloat16 *src = p.x + static_cast<size_t>(m0 + tok) * p.K + static_cast<size_t>(c) * kW4BlockK + (tid & 15) * 8;
+                const uint32_t dst = raw + n * (8 * kRawTok);
+#pragma unroll
+                for (int b = 0; b < kW4Chunk; ++b)
+                    if (b < nblk) {
+                        const bool ok = b * kW4BlockK < left;
+                        w4::cp16(dst + b * 256, ok ? src + b * kW4BlockK : p.x, ok ? 16u : 0u);
+                    }
+            }
+        }
+        // scales and zero points; scales of groups past K: zero
+        for (int i = tid; i < nblk * kGroups * 16; i += kW4Threads) {
+            const int j = i >> 4, q = i & 15;
+            if (q * 8 < rows_left) {
+                const int grp = c * kGroups + j;
+                const bool ok = grp < static_cast<int>(groups);
+                const size_t at = static_cast<size_t>(ok ? grp : 0) * p.N + q * 8;
+                w4::cp16(s_base + L::s_offset(p.tok_cap) + buf * (kW4Chunk * L::kSBlock) + j * (kW4Rows * 2) + q * 16,
+                         sc + at, ok ? 16u : 0u);
+                if (kZeros)
+                    w4::cp8(s_base + L::z_offset(p.tok_cap, p.bufs) + buf * (kW4Chunk * L::kZBlock) + j * kW4Rows + q * 8, zp + at);
+            }
+        }
+    };
+
+    // this thread's pieces of x to where the products want them, in pair order
+    auto pair = [&](int nblk) {
+#pragma unroll
+        for (int n = 0; n < kNT; ++n) {
+            const int tok = 8 * n + (tid >> 4);
+            if (tok < ntok) {
+                const uint32_t src = raw + n * (8 * kRawTok);
+                const uint32_t dst = s_base + L::kXOffset + tok * kW4XPitch + w4::x_slot<kGs>(tid & 15) * 16;
+#pragma unroll
+                for (int b = 0; b < kW4Chunk; ++b)
+                    if (b < nblk) {
+                        const uint4 v = w4::lds128(src + b * 256);
+                        w4::sts128(dst + b * 256, make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
+                                                             __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632)));
+                    }
+            }
+        }
+    };
+
+    // where this lane's rows of x lie: tokens past the run's read zeros
+    uint32_t xa[kNT];
 #pragma unroll
     for (int n = 0; n < kNT; ++n)
-        xrow[n] = (8 * n + g8 < ntok ? s_base + L::kXOffset + (8 * n + g8) * x_pitch : zero_row) + t4 * 16;
+        xa[n] = (8 * n + g8 < ntok ? s_base + L::kXOffset + (8 * n + g8) * kW4XPitch : zero_row) + t4 * 16;
 #pragma unroll
     for (int i = 0; i < 4; ++i) wptr[i] = wrow[i] + static_cast<size_t>(blk0) * (kW4BlockK / 2);
+    stage(blk0, 0);
+    w4::cp_commit();
 #pragma unroll
     for (int d = 0; d < kW4Depth; ++d) copy(blk0 + d, d, d * (kW4BlockK / 2));
+    w4::cp_wait<kW4Depth>();                       // the first chunk has landed
 
-    for (int c0 = blk0; c0 < blk1; c0 += p.chunk) {
-        const int c1 = min(c0 + p.chunk, blk1);
-        if (c0 != blk0) __syncthreads();       // the chunk before has been read
-        // scales and zero points; groups past K: zero
-        for (int i = tid; i < (c1 - c0) * kGroups * 16; i += kW4Threads) {
-            const int j = i >> 4, c = i & 15;
-            if (c * 8 < rows_left) {
-                const int grp = c0 * kGroups + j;
-                const bool ok = grp < static_cast<int>(groups);
-                const size_t at = static_cast<size_t>(ok ? grp : 0) * p.N + c * 8;
-                w4::cp16(s_base + L::s_offset(p.tok_cap, p.chunk) + j * (kW4Rows * 2) + c * 16, sc + at, ok ? 16u : 0u);
-                if (kZeros) w4::cp8(s_base + L::z_offset(p.tok_cap, p.chunk) + j * kW4Rows + c * 8, zp + at);
-            }
-        }
+    int buf = 0;
+    for (int c0 = blk0; c0 < blk1; c0 += kW4Chunk) {
+        if (c0 != blk0) __syncthreads();           // the chunk before has been read
+        pair(min(kW4Chunk, blk1 - c0));
+        __syncthreads();
+        if (c0 + kW4Chunk < blk1) stage(c0 + kW4Chunk, buf ^ 1);
         w4::cp_commit();
-        // x, 8 values at a time, in the products' order; zeros past K.  Thread: piece
-        // tid % 16 of each block, tokens tid / 16, tid / 16 + 8, ...
-        {
-            const int c = tid & 15;
-            const int have = (p.K - c0 * kW4BlockK - c * 8 + kW4BlockK - 1) / kW4BlockK;   // blocks whose piece lies below K
+        const uint32_t sa = s_off + buf * (kW4Chunk * L::kSBlock), za = z_off + buf * (kW4Chunk * L::kZBlock);
 #pragma unroll
-            for (int n = 0; n < kNT; ++n) {
-                const int tok = 8 * n + (tid >> 4);
-                if (tok < ntok) {
-                    const uint4 *src = reinterpret_cast<const uint4 *>(
-                        p.x + static_cast<size_t>(m0 + tok) * p.K + static_cast<size_t>(c0) * kW4BlockK) + c;
-                    uint32_t dst = s_base + L::kXOffset + tok * x_pitch + w4::x_slot<kGs>(c) * 16;
-#pragma unroll 4
-                    for (int b = 0; b < c1 - c0; ++b) {
-                        const uint4 v = b < have ? __ldg(src + b * 16) : make_uint4(0u, 0u, 0u, 0u);
-                        w4::sts128(dst + b * 256,
-                                   make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
-                                              __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632)));
+        for (int u = 0; u < kW4Chunk; ++u) {
+            if (c0 + u >= blk1) break;
+            // this block's copies have landed: behind them are those of the next block
+            // and, until kW4Depth blocks of the chunk are done, the next chunk's (which
+            // has landed, too, when the last wait of four is over)
+            if (u < kW4Depth) w4::cp_wait<kW4Depth>();
+            else w4::cp_wait<kW4Depth - 1>();
+            __syncwarp();                      // of every lane
+#pragma unroll
+            for (int j = 0; j < kGroups; ++j) {
+                uint32_t zero[4] = {0x43084308u, 0x43084308u, 0x43084308u, 0x43084308u};
+                if constexpr (kZeros) {
+                    const uint32_t zb = w4::lds32(za + u * L::kZBlock + j * kW4Rows) & 0x7F7F7F7Fu;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) zero[i] = __byte_perm(zb, 0x43u, 0x4040 + i * 0x0101);   // 128 + z
+                }
+                uint32_t w[4][kWords];
+                const uint32_t wa = (w_read ^ (j * (64 / kGroups))) + u % kW4Depth * kW4WarpBlock;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if constexpr (kGs == 128) {
+                        const uint4 v = w4::lds128(wa + i * 512);
+                        w[i][0] = v.x; w[i][1] = v.y; w[i][2] = v.z; w[i][3] = v.w;
+                    } else if constexpr (kGs == 64) {
+                        const uint2 v = w4::lds64(wa + i * 512);
+                        w[i][0] = v.x; w[i][1] = v.y;
+                    } else {
+                        w[i][0] = w4::lds32(wa + i * 512);
                     }
                 }
-            }
-        }
-        w4::cp_wait<0>();
-        __syncthreads();
-        uint32_t xa[kNT], sa = s_off, za = z_off;
+                float c[2][kNT][4];
 #pragma unroll
-        for (int n = 0; n < kNT; ++n) xa[n] = xrow[n];
-        // a chunk starts at a multiple of kW4Depth blocks from blk0: block b0 + u lies in slot u
-        for (int b0 = c0; b0 < c1; b0 += kW4Depth) {
+                for (int k = 0; k < kWords; ++k) {
+                    uint4 x[kNT];
 #pragma unroll
-            for (int u = 0; u < kW4Depth; ++u) {
-                if (b0 + u >= c1) break;
-                w4::cp_wait<kW4Depth - 1>();
-                __syncwarp();                  // every lane's copies of this block have landed
+                    for (int n = 0; n < kNT; ++n) x[n] = w4::lds128(xa[n] + u * 256 + (j * kWords + k) * 64);
 #pragma unroll
-                for (int j = 0; j < kGroups; ++j) {
-                    uint32_t zero[4] = {0x43084308u, 0x43084308u, 0x43084308u, 0x43084308u};
-                    if constexpr (kZeros) {
-                        const uint32_t zb = w4::lds32(za + u * L::kZBlock + j * kW4Rows) & 0x7F7F7F7Fu;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) zero[i] = __byte_perm(zb, 0x43u, 0x4040 + i * 0x0101);   // 128 + z
-                    }
-                    uint32_t w[4][kWords];
-                    const uint32_t wa = (w_read ^ (j * (64 / kGroups))) + u * kW4WarpBlock;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if constexpr (kGs == 128) {
-                            const uint4 v = w4::lds128(wa + i * 512);
-                            w[i][0] = v.x; w[i][1] = v.y; w[i][2] = v.z; w[i][3] = v.w;
-                        } else if constexpr (kGs == 64) {
-                            const uint2 v = w4::lds64(wa + i * 512);
-                            w[i][0] = v.x; w[i][1] = v.y;
-                        } else {
-                            w[i][0] = w4::lds32(wa + i * 512);
-                        }
-                    }
-                    float c[2][kNT][4];
-#pragma unroll
-                    for (int k = 0; k < kWords; ++k) {
-                        uint4 x[kNT];
-#pragma unroll
-                        for (int n = 0; n < kNT; ++n) x[n] = w4::lds128(xa[n] + u * 256 + (j * kWords + k) * 64);
-#pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            const uint32_t lo = w[2 * r][k], hi = w[2 * r + 1][k];
-                            const uint32_t zl = zero[2 * r], zh = zero[2 * r + 1];
-                            const uint32_t l0 = w4::codes<0>(lo, bias, zl), l1 = w4::codes<1>(lo, bias, zl),
-                                           l2 = w4::codes<2>(lo, bias, zl), l3 = w4::codes<3>(lo, bias, zl);
-                            const uint32_t h0 = w4::codes<0>(hi, bias, zh), h1 = w4::codes<1>(hi, bias, zh),
-                                           h2 = w4::codes<2>(hi, bias, zh), h3 = w4::codes<3>(hi, bias, zh);
-#pragma unroll
-                            for (int n = 0; n < kNT; ++n) {
-                                if (k == 0) w4::mma_first(c[r][n], l0, h0, l1, h1, x[n].x, x[n].y);
-                                else w4::mma(c[r][n], l0, h0, l1, h1, x[n].x, x[n].y);
-                                w4::mma(c[r][n], l2, h2, l3, h3, x[n].z, x[n].w);
-                            }
-                        }
-                    }
-                    const uint2 sv = w4::lds64(sa + u * L::kSBlock + j * (kW4Rows * 2));
-                    const float s4[4] = {__uint_as_float(sv.x << 16), __uint_as_float(sv.x & 0xFFFF0000u),
-                                         __uint_as_float(sv.y << 16), __uint_as_float(sv.y & 0xFFFF0000u)};
-#pragma unroll
-                    for (int r = 0; r < 2; ++r)
+                    for (int r = 0; r < 2; ++r) {
+                        const uint32_t lo = w[2 * r][k], hi = w[2 * r + 1][k];
+                        const uint32_t zl = zero[2 * r], zh = zero[2 * r + 1];
+                        const uint32_t l0 = w4::codes<0>(lo, bias, zl), l1 = w4::codes<1>(lo, bias, zl),
+                                       l2 = w4::codes<2>(lo, bias, zl), l3 = w4::codes<3>(lo, bias, zl);
+                        const uint32_t h0 = w4::codes<0>(hi, bias, zh), h1 = w4::codes<1>(hi, bias, zh),
+                                       h2 = w4::codes<2>(hi, bias, zh), h3 = w4::codes<3>(hi, bias, zh);
 #pragma unroll
                         for (int n = 0; n < kNT; ++n) {
-                            acc[r][n][0] = fmaf(s4[2 * r], c[r][n][0], acc[r][n][0]);
-                            acc[r][n][1] = fmaf(s4[2 * r], c[r][n][1], acc[r][n][1]);
-                            acc[r][n][2] = fmaf(s4[2 * r + 1], c[r][n][2], acc[r][n][2]);
-                            acc[r][n][3] = fmaf(s4[2 * r + 1], c[r][n][3], acc[r][n][3]);
+                            if (k == 0) w4::mma_first(c[r][n], l0, h0, l1, h1, x[n].x, x[n].y);
+                            else w4::mma(c[r][n], l0, h0, l1, h1, x[n].x, x[n].y);
+                            w4::mma(c[r][n], l2, h2, l3, h3, x[n].z, x[n].w);
                         }
+                    }
                 }
-                __syncwarp();                  // every lane has read this block
-                copy(b0 + u + kW4Depth, u, (u + kW4Depth) * (kW4BlockK / 2));
+                const uint2 sv = w4::lds64(sa + u * L::kSBlock + j * (kW4Rows * 2));
+                const float s4[4] = {__uint_as_float(sv.x << 16), __uint_as_float(sv.x & 0xFFFF0000u),
+                                     __uint_as_float(sv.y << 16), __uint_as_float(sv.y & 0xFFFF0000u)};
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+#pragma unroll
+                    for (int n = 0; n < kNT; ++n) {
+                        acc[r][n][0] = fmaf(s4[2 * r], c[r][n][0], acc[r][n][0]);
+                        acc[r][n][1] = fmaf(s4[2 * r], c[r][n][1], acc[r][n][1]);
+                        acc[r][n][2] = fmaf(s4[2 * r + 1], c[r][n][2], acc[r][n][2]);
+                        acc[r][n][3] = fmaf(s4[2 * r + 1], c[r][n][3], acc[r][n][3]);
+                    }
             }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) wptr[i] += kW4Depth * (kW4BlockK / 2);
-#pragma unroll
-            for (int n = 0; n < kNT; ++n) xa[n] += kW4Depth * 256;
-            sa += kW4Depth * L::kSBlock;
-            za += kW4Depth * L::kZBlock;
+            __syncwarp();                  // every lane has read this block
+            copy(c0 + u + kW4Depth, u % kW4Depth, (u + kW4Depth) * (kW4BlockK / 2));
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) wptr[i] += kW4Chunk * (kW4BlockK / 2);
+        buf ^= 1;
     }
     // This lane's sums of 4 rows for 2 kNT tokens go to the rows' owner: rank
     // r adds rows 128 r / split .. and keeps [source rank][token][its rows].
