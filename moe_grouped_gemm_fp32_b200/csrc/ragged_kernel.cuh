@@ -236,8 +236,7 @@ __device__ __forceinline__ void add8(__nv_bfloat16 *d, const float *v) {
 // A warp's way from accumulator rows (one a lane) to runs of a row in memory, 32
 // columns at a time: `put` writes a box of 32 rows to shared memory, its 16-byte
 // pieces permuted by the row against bank conflicts, and stores it in runs of 64 (BF16)
-// or 128 bytes of a row.  Addresses that do not change are kept: the epilogue's
-// instructions are what bounds tiles with few products.
+// or 128 bytes of a row.  Addresses that do not change are kept.
 template <bool kF32>
 struct BoxWriter {
     static constexpr int kElem = kF32 ? 4 : 2;
@@ -317,7 +316,6 @@ struct BoxWriter {
 };
 
 // tm_a, tm_b: see the operand table above (kNT, kNN single-CTA: A boxes of 32 rows).
-// tm_d: boxes of 32 columns by 32 rows of D [groups][rows][N] (kTN: one group per expert).
 // kRows: rows of a CTA's tile (32 or 128).
 template <int kDir, int kBN, int kStages, int kCtaGroup, bool kF32, int kRows>
 __global__ void __launch_bounds__(ragged_threads(kF32), 1)
