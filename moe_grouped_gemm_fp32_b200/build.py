@@ -16,7 +16,7 @@ CSRC = os.path.join(HERE, "csrc")
 SOURCES = [os.path.join(CSRC, f) for f in ("dg_api.cu", "quant_api.cu", "bf16_api.cu",
                                               "ragged_api.cu", "w4_api.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("gemm_kernel.cuh", "ptx.cuh", "quant_kernel.cuh",
-                                                  "bf16_kernel.cuh", "ragged_kernel.cuh", "w4_kernel.cuh",
+                                                  "bf16_kernel.cuh", "ragged_kernel.cuh", "w4_kernel.cuh", "pdl.cuh",
                                                   "api_common.h")] + [
     os.path.join(ROOT, "include", "dg.h")]
 OUT = os.path.join(HERE, "_dg.so")

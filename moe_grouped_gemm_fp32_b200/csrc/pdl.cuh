@@ -1,0 +1,18 @@
+// pdl.cuh -- programmatic dependent launch: a kernel launched with the attribute
+// may start while the kernel before it in the stream ends.  Nothing that depends
+// on that kernel may be read, and nothing written, before grid_dependency_wait();
+// every block calls it, also one without work, so that a grid's end implies the
+// end of all before it.
+#pragma once
+
+namespace dg {
+namespace pdl {
+
+// All grids this one depends on have completed and their writes are visible.
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// The next grid may be scheduled once every block has called this (or ended).
+__device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+}  // namespace pdl
+}  // namespace dg

@@ -42,13 +42,15 @@ struct Launch {
         cfg.dynamicSmemBytes = L::kAlloc;
         cfg.stream = stream;
         cfg.attrs = attr;
-        cfg.numAttrs = 0;
+        cfg.numAttrs = 1;
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;      // see pdl.cuh
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
         if (kCtaGroup > 1) {
-            attr[0].id = cudaLaunchAttributeClusterDimension;
-            attr[0].val.clusterDim.x = kCtaGroup;
-            attr[0].val.clusterDim.y = 1;
-            attr[0].val.clusterDim.z = 1;
-            cfg.numAttrs = 1;
+            attr[1].id = cudaLaunchAttributeClusterDimension;
+            attr[1].val.clusterDim.x = kCtaGroup;
+            attr[1].val.clusterDim.y = 1;
+            attr[1].val.clusterDim.z = 1;
+            cfg.numAttrs = 2;
         }
     }
 
@@ -70,7 +72,7 @@ struct Launch {
         int n = info->num_sms;
         if (kCtaGroup > 1) {
             cudaLaunchConfig_t cfg;
-            cudaLaunchAttribute attr[1];
+            cudaLaunchAttribute attr[2];
             config(cfg, attr, kCtaGroup, nullptr);
             if ((e = cudaOccupancyMaxActiveClusters(&n, kernel(), &cfg)) != cudaSuccess)
                 return cuda_fail(e, "cudaOccupancyMaxActiveClusters(ragged)");
@@ -92,7 +94,7 @@ struct Launch {
             std::fprintf(stderr, "[dg] ragged dir=%d rows=%d bn=%d stages=%d ctas/mma=%d f32=%d grid=%d smem=%d\n", kDir,
                          kRows, kBN, kStages, kCtaGroup, kF32 ? 1 : 0, grid, L::kAlloc);
         cudaLaunchConfig_t cfg;
-        cudaLaunchAttribute attr[1];
+        cudaLaunchAttribute attr[2];
         config(cfg, attr, grid, stream);
         cudaError_t e = cudaLaunchKernelEx(&cfg, kernel(), ma, mb, p);
         return e == cudaSuccess ? DG_SUCCESS : cuda_fail(e, "ragged_gemm_kernel launch");

@@ -59,6 +59,7 @@
 #pragma once
 
 #include "gemm_kernel.cuh"
+#include "pdl.cuh"
 
 namespace dg {
 
@@ -375,6 +376,9 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
         *abort_flag = 0;
         ptx::fence_mbar_init();
     }
+    // The launch may overlap the end of the kernel before it in the stream: from here on
+    // that kernel is done and its writes are visible.
+    pdl::grid_dependency_wait();
     if (warp == kEpiWarp0) {
         // offsets as the tiles use them: clamped to [0, T] and made non-decreasing.  Four
         // of them a lane, so that their loads are in flight together.
@@ -719,6 +723,10 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
             }
         }
     }
+
+    // The next grid's blocks may be placed: a block that comes earlier, on the SMs that
+    // are done first, would find the SMs unevenly filled.
+    pdl::grid_launch_dependents();
 
     // ---------------------------------------------------------------- teardown
     if (warp == 1 && ptx::elect_one()) {

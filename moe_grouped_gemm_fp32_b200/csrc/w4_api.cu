@@ -52,13 +52,15 @@ dg_status_t launch_w4(dg::W4Params p, int split, int runs, cudaStream_t stream) 
     cfg.blockDim = dim3(dg::kW4Threads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = split;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;      // see pdl.cuh
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = split;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = split > 1 ? 1 : 0;
+    cfg.numAttrs = split > 1 ? 2 : 1;
     if (verbose())
         std::fprintf(stderr, "[dg] w4_gemv group=%d tokens=%d split=%d grid=%ux%ux%u bufs=%d smem=%d\n", kGs, 8 * kNT,
                      split, cfg.gridDim.x, cfg.gridDim.y, cfg.gridDim.z, p.bufs, smem);

@@ -41,6 +41,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "pdl.cuh"
 #include "ptx.cuh"
 
 namespace dg {
@@ -254,6 +255,9 @@ w4_gemv_kernel(const W4Params p) {
     const int split = static_cast<int>(gridDim.x), rank = static_cast<int>(blockIdx.x);
     const int n0 = static_cast<int>(blockIdx.y) * kW4Rows;
 
+    // The launch may overlap the end of the kernel before it in the stream: from here on
+    // that kernel is done and its writes are visible.
+    pdl::grid_dependency_wait();
     int expert = 0, first = static_cast<int>(blockIdx.z) * kTok, end = min(p.M, first + kTok);
     if (p.offsets) {
         const int z = static_cast<int>(blockIdx.z);

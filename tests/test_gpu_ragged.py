@@ -358,3 +358,54 @@ def test_large_offsets_pass_32_bits():
     assert torch.equal(d[T - 260:T - 250], (x[T - 260:T - 250].double() @ w[0].double().t()).to(BF16))
     assert torch.equal(d[T - 250:], (x[T - 250:].double() @ w[1].double().t()).to(BF16))
     assert not d[T - 400:T - 260].any()
+
+
+@pytest.mark.parametrize("graph", [False, True])
+def test_dependent_calls_in_a_row(graph):
+    """Each call reads what the one before it wrote, and writes what an earlier one
+    read; launches that overlap must give what calls with a wait between them give."""
+    torch.manual_seed(3)
+    T, H, I, G = 96, 512, 1024, 6
+    off = _dev([0, 20, 20, 50, 51, 90, 96])
+    w1 = (torch.randn(G, I, H, device="cuda") * H ** -0.5).to(BF16)
+    w2 = (torch.randn(G, H, I, device="cuda") * I ** -0.5).to(BF16)
+    codes = torch.randint(0, 256, (H, H // 2), device="cuda").to(torch.uint8)
+    scales = (torch.rand(H // 64, H, device="cuda") * 0.01).to(BF16)
+    start = torch.randn(T, H, device="cuda", dtype=BF16)
+    x, y, z = (torch.empty(T, n, device="cuda", dtype=BF16) for n in (H, I, H))
+    dw = torch.empty(G, I, H, device="cuda", dtype=F32)
+
+    def chain(wait):
+        x.copy_(start)
+        dw.zero_()
+        for _ in range(8):
+            dg.dg_m_grouped_bf16_gemm_nt_ragged(x, w1, y, off)
+            wait()
+            dg.dg_k_grouped_bf16_gemm_tn_ragged(y, x, dw, off, accumulate=True)
+            wait()
+            dg.dg_m_grouped_bf16_gemm_nt_ragged(y, w2, z, off)
+            wait()
+            dg.dg_w4_gemv_nt(z, codes, scales, x)
+            wait()
+            dg.dg_m_grouped_bf16_gemm_nn_ragged(y, w1, z, off)
+            wait()
+            x.add_(z)
+            wait()
+
+    chain(torch.cuda.synchronize)
+    want = [t.clone() for t in (x, y, z, dw)]
+    if graph:
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.stream(s):
+            with torch.cuda.graph(g, stream=s):
+                chain(lambda: None)
+        torch.cuda.current_stream().wait_stream(s)
+    for _ in range(5):
+        for t in (x, y, z, dw):
+            t.fill_(float("nan"))
+        g.replay() if graph else chain(lambda: None)
+        torch.cuda.synchronize()
+        for got, ref in zip((x, y, z, dw), want):
+            assert torch.equal(got, ref)
