@@ -44,9 +44,11 @@
 // that weight bytes, not token tiles, fill the memory pipeline.  Where experts have
 // a few rows, tiles are thin (kRows 32): a stage keeps 4 KB for A and not 16, and
 // twice as many weight bytes are in flight (64 rows over 16 experts, 4096 x 7168: 156
-// -> 143 us, 98 % of the copy rate).  The MMA still has 128 rows; rows 32 and
-// on read whatever follows in shared memory (B, the next stage, in the middle of
-// being written perhaps) and give accumulator rows that nobody reads.
+// -> 143 us, 98 % of the copy rate).  There the weights are the MMA's 128 rows and the
+// tokens its 32 columns: the other way round, three quarters of the products or more
+// would be of rows that no expert has (XX).  Tiles of 64 weights leave the MMA's upper
+// rows whatever follows in shared memory (the next stage, in the middle of being
+// written perhaps); nobody reads those accumulator rows.
 //
 // Precision.  The tensor core's FP32 accumulator truncates: measured against 64
 // bits, a sum of 8192 products loses 9e-6 (relative, 2-norm) and 32768 products
@@ -110,7 +112,9 @@ struct RaggedSmem {
     static constexpr int kOutOffset = (kPrefixOffset + (kMaxGroups + 1) * 4 + 1023) / 1024 * 1024;
     static constexpr int kUsed = kOutOffset + (ragged_threads(kF32) / 32 - 4) * kBoxBytes;
     static constexpr int kAlloc = (kUsed + 1024 > kMinSmem) ? kUsed + 1024 : kMinSmem;
-    static constexpr int kTmemCols = kAccBufs * kBN <= 128 ? 128 : kAccBufs * kBN <= 256 ? 256 : 512;
+    static constexpr int kAccCols = kRows == 32 ? 32 : kBN;          // thin tiles: the tokens
+    static constexpr int kTmemCols = kAccBufs * kAccCols <= 128 ? kAccBufs * kAccCols
+                                     : kAccBufs * kAccCols <= 256 ? 256 : 512;
     static_assert(kBN == 64 || kBN == 128 || kBN == 256, "tile N");
     static_assert(kBCols % 64 == 0, "MN-major boxes are 64 columns wide");
     static_assert(kAlloc <= 227 * 1024, "shared memory budget");
@@ -326,8 +330,9 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
     using Tile = RaggedTile<kDir, kBN, kCtaGroup, kRows>;
     static_assert(!kF32 || kDir == kTN, "FP32 output: weight gradient");
     static_assert(kRows == kTileX || (kRows == 32 && kDir != kTN && kCtaGroup == 1), "thin tiles: one CTA, K-major A");
-    // a thin tile's A descriptor runs on over 96 rows' bytes that follow its 32
-    static_assert(kTileX * 128 <= L::kStageBytes + (L::kUsed - L::kBarOffset), "A reads stay inside shared memory");
+    constexpr bool kThin = kRows == 32;
+    // the weight descriptor of a thin tile of 64 runs on over as many rows that follow
+    static_assert(!kThin || kTileX * 128 - L::kBBytes <= L::kUsed - L::kBarOffset, "reads stay inside shared memory");
     constexpr bool kPair = kCtaGroup == 2;
     constexpr bool kAMn = kDir == kTN, kBMn = kDir != kNT;
     constexpr int kAccBufs = L::kAccBufs;
@@ -549,7 +554,8 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
                 int stage = 0, buf = 0;
                 uint32_t phase = 0, tphase = 0;
                 bool ok = true;
-                const uint32_t idesc = ragged_idesc(kTileX * kCtaGroup, kBN, kAMn, kBMn);
+                const uint32_t idesc = kThin ? ragged_idesc(kTileX, 32, kBMn, kAMn)
+                                             : ragged_idesc(kTileX * kCtaGroup, kBN, kAMn, kBMn);
                 constexpr uint32_t kStepA = kAMn ? 2048 >> 4 : 32 >> 4;   // 16 reduced indices
                 constexpr uint32_t kStepB = kBMn ? 2048 >> 4 : 32 >> 4;
                 Tile tl;
@@ -561,7 +567,7 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
                     for (int kb0 = 0; ok && kb0 < max(tl.num_kb, 1); kb0 += seg) {
                         if (!wait(tempty_bar(buf), tphase ^ 1u, kSiteMmaTmemEmpty)) { ok = false; break; }
                         ptx::tc_fence_after();
-                        const uint32_t dtm = tmem_base + static_cast<uint32_t>(buf * kBN);
+                        const uint32_t dtm = tmem_base + static_cast<uint32_t>(buf * L::kAccCols);
                         const int kb1 = min(kb0 + seg, tl.num_kb);
                         for (int kb = kb0; kb < kb1; kb += L::kSub) {
                             if (!wait(full_bar(stage), phase, kSiteMmaFull)) { ok = false; break; }
@@ -578,6 +584,7 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
                                     if (k < steps) {
                                         const uint32_t acc = (kb > kb0 || s > 0 || k > 0) ? 1u : 0u;
                                         if constexpr (kPair) ptx::mma_f16_pair(dtm, da + kStepA * k, db + kStepB * k, idesc, acc);
+                                        else if constexpr (kThin) ptx::mma_f16(dtm, db + kStepB * k, da + kStepA * k, idesc, acc);
                                         else ptx::mma_f16(dtm, da + kStepA * k, db + kStepB * k, idesc, acc);
                                     }
                                 }
@@ -658,6 +665,36 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
         const int e_step = kPromote ? t_step : 2 * t_step;
         for (int t = t_first + group * t_step; ok && t < num_tiles; t += e_step) {
             tl.decode(t, p, offs, prefix);
+            if constexpr (kThin) {
+                // lanes are weights, columns tokens: a warp turns 32 weights by 16 tokens round
+                if (!wait(tfull_bar(buf), tphase, kSitePromoFull)) { ok = false; break; }
+                ptx::tc_fence_after();
+                float v[16];
+                ptx::tmem_ld16(tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
+                               static_cast<uint32_t>(buf * L::kAccCols + half * 16), v);
+                ptx::tmem_wait_ld();
+                release();
+                const int tokens = min(tl.row_end - tl.row0, kRows) - half * 16;      // of the warp's 16
+                const int n = tl.n0 + quarter * 32;
+                if (quarter * 32 < kBN && n < p.N && tokens > 0) {
+                    uint8_t *box = smem + L::kOutOffset + (warp - kEpiWarp0) * L::kBoxBytes;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        *reinterpret_cast<__nv_bfloat16 *>(box + j * 64 + lane * 2) = __float2bfloat16_rn(v[j]);
+                    __syncwarp();
+                    const int piece = lane % 4 * 8;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int tok = i * 8 + lane / 4;
+                        const uint4 x = *reinterpret_cast<const uint4 *>(box + tok * 64 + piece * 2);
+                        if (tok < tokens && n + piece < p.N)
+                            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.d) +
+                                                       static_cast<size_t>(tl.row0 + half * 16 + tok) * p.N + n + piece) = x;
+                    }
+                    __syncwarp();
+                }
+                continue;
+            }
             const int rows = min(tl.row_end, tl.row0 + pair_rank * kTileX + kRows) - (tl.row0 + wrow);   // of the warp's 32
             const int c0 = tl.n0 + half * kHalf;
             const size_t row0 = (kDir == kTN ? static_cast<size_t>(tl.g) * p.M : 0) + tl.row0 + wrow;
