@@ -44,11 +44,14 @@
 // that weight bytes, not token tiles, fill the memory pipeline.  Where experts have
 // a few rows, tiles are thin (kRows 32): a stage keeps 4 KB for A and not 16, and
 // twice as many weight bytes are in flight (64 rows over 16 experts, 4096 x 7168: 156
-// -> 143 us, 98 % of the copy rate).  There the weights are the MMA's 128 rows and the
-// tokens its 32 columns: the other way round, three quarters of the products or more
-// would be of rows that no expert has (XX).  Tiles of 64 weights leave the MMA's upper
-// rows whatever follows in shared memory (the next stage, in the middle of being
-// written perhaps); nobody reads those accumulator rows.
+// -> 143 us, 98 % of the copy rate).
+//
+// Single CTAs of kNT and kNN make the weights the MMA's 128 rows and the tokens its
+// columns, as many as the expert has, rounded up to 16: the other way round, products
+// of rows that no expert has cost time and, in a loop, the clock (those 64 rows: 165 ->
+// 141 us; 64 experts of 62 rows on average, 1000 x 2112: 66 -> 61).  Tiles of 64 weights leave
+// the MMA's upper rows whatever follows in shared memory (the next stage, in the middle
+// of being written perhaps); nobody reads those accumulator rows.
 //
 // Precision.  The tensor core's FP32 accumulator truncates: measured against 64
 // bits, a sum of 8192 products loses 9e-6 (relative, 2-norm) and 32768 products
@@ -112,7 +115,8 @@ struct RaggedSmem {
     static constexpr int kOutOffset = (kPrefixOffset + (kMaxGroups + 1) * 4 + 1023) / 1024 * 1024;
     static constexpr int kUsed = kOutOffset + (ragged_threads(kF32) / 32 - 4) * kBoxBytes;
     static constexpr int kAlloc = (kUsed + 1024 > kMinSmem) ? kUsed + 1024 : kMinSmem;
-    static constexpr int kAccCols = kRows == 32 ? 32 : kBN;          // thin tiles: the tokens
+    static constexpr bool kSwap = kDir != kTN && kCtaGroup == 1;     // weights are rows, tokens columns
+    static constexpr int kAccCols = kSwap ? kRows : kBN;
     static constexpr int kTmemCols = kAccBufs * kAccCols <= 128 ? kAccBufs * kAccCols
                                      : kAccBufs * kAccCols <= 256 ? 256 : 512;
     static_assert(kBN == 64 || kBN == 128 || kBN == 256, "tile N");
@@ -330,9 +334,9 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
     using Tile = RaggedTile<kDir, kBN, kCtaGroup, kRows>;
     static_assert(!kF32 || kDir == kTN, "FP32 output: weight gradient");
     static_assert(kRows == kTileX || (kRows == 32 && kDir != kTN && kCtaGroup == 1), "thin tiles: one CTA, K-major A");
-    constexpr bool kThin = kRows == 32;
-    // the weight descriptor of a thin tile of 64 runs on over as many rows that follow
-    static_assert(!kThin || kTileX * 128 - L::kBBytes <= L::kUsed - L::kBarOffset, "reads stay inside shared memory");
+    constexpr bool kSwap = L::kSwap;
+    // the weight descriptor of a tile of 64 runs on over as many rows that follow
+    static_assert(!kSwap || kTileX * 128 - L::kBBytes <= L::kUsed - L::kBarOffset, "reads stay inside shared memory");
     constexpr bool kPair = kCtaGroup == 2;
     constexpr bool kAMn = kDir == kTN, kBMn = kDir != kNT;
     constexpr int kAccBufs = L::kAccBufs;
@@ -554,13 +558,14 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
                 int stage = 0, buf = 0;
                 uint32_t phase = 0, tphase = 0;
                 bool ok = true;
-                const uint32_t idesc = kThin ? ragged_idesc(kTileX, 32, kBMn, kAMn)
-                                             : ragged_idesc(kTileX * kCtaGroup, kBN, kAMn, kBMn);
                 constexpr uint32_t kStepA = kAMn ? 2048 >> 4 : 32 >> 4;   // 16 reduced indices
                 constexpr uint32_t kStepB = kBMn ? 2048 >> 4 : 32 >> 4;
                 Tile tl;
                 for (int t = t_first; ok && t < num_tiles; t += t_step) {
                     tl.decode(t, p, offs, prefix);
+                    const int columns = (min(tl.row_end - tl.row0, kRows) + 15) / 16 * 16;
+                    const uint32_t idesc = kSwap ? ragged_idesc(kTileX, columns, kBMn, kAMn)
+                                                 : ragged_idesc(kTileX * kCtaGroup, kBN, kAMn, kBMn);
                     // one accumulator for the tile (nothing in it for an expert without tokens), or
                     // one for each segment
                     const int seg = kPromote ? kSegBlocks : max(tl.num_kb, 1);
@@ -584,7 +589,7 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
                                     if (k < steps) {
                                         const uint32_t acc = (kb > kb0 || s > 0 || k > 0) ? 1u : 0u;
                                         if constexpr (kPair) ptx::mma_f16_pair(dtm, da + kStepA * k, db + kStepB * k, idesc, acc);
-                                        else if constexpr (kThin) ptx::mma_f16(dtm, db + kStepB * k, da + kStepA * k, idesc, acc);
+                                        else if constexpr (kSwap) ptx::mma_f16(dtm, db + kStepB * k, da + kStepA * k, idesc, acc);
                                         else ptx::mma_f16(dtm, da + kStepA * k, db + kStepB * k, idesc, acc);
                                     }
                                 }
@@ -665,34 +670,39 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
         const int e_step = kPromote ? t_step : 2 * t_step;
         for (int t = t_first + group * t_step; ok && t < num_tiles; t += e_step) {
             tl.decode(t, p, offs, prefix);
-            if constexpr (kThin) {
+            if constexpr (kSwap) {
                 // lanes are weights, columns tokens: a warp turns 32 weights by 16 tokens round
                 if (!wait(tfull_bar(buf), tphase, kSitePromoFull)) { ok = false; break; }
                 ptx::tc_fence_after();
-                float v[16];
-                ptx::tmem_ld16(tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
-                               static_cast<uint32_t>(buf * L::kAccCols + half * 16), v);
-                ptx::tmem_wait_ld();
-                release();
-                const int tokens = min(tl.row_end - tl.row0, kRows) - half * 16;      // of the warp's 16
+                const int first = half * (kRows / 2);                  // of the warp's tokens
+                const int tokens = min(tl.row_end - tl.row0 - first, kRows / 2);
                 const int n = tl.n0 + quarter * 32;
-                if (quarter * 32 < kBN && n < p.N && tokens > 0) {
+                if (quarter * 32 < kBN && n < p.N) {
                     uint8_t *box = smem + L::kOutOffset + (warp - kEpiWarp0) * L::kBoxBytes;
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        *reinterpret_cast<__nv_bfloat16 *>(box + j * 64 + lane * 2) = __float2bfloat16_rn(v[j]);
-                    __syncwarp();
                     const int piece = lane % 4 * 8;
+                    uint8_t *dst = static_cast<uint8_t *>(p.d) +
+                                   (static_cast<size_t>(tl.row0 + first + lane / 4) * p.N + n + piece) * 2;
+                    const size_t step = static_cast<size_t>(p.N) * 16;                 // 8 tokens
+#pragma unroll 1
+                    for (int c = 0; c < tokens; c += 16) {
+                        float v[16];
+                        ptx::tmem_ld16(tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
+                                       static_cast<uint32_t>(buf * L::kAccCols + first + c), v);
+                        ptx::tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int tok = i * 8 + lane / 4;
-                        const uint4 x = *reinterpret_cast<const uint4 *>(box + tok * 64 + piece * 2);
-                        if (tok < tokens && n + piece < p.N)
-                            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.d) +
-                                                       static_cast<size_t>(tl.row0 + half * 16 + tok) * p.N + n + piece) = x;
+                        for (int j = 0; j < 16; ++j)
+                            *reinterpret_cast<__nv_bfloat16 *>(box + j * 64 + lane * 2) = __float2bfloat16_rn(v[j]);
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const uint4 x = *reinterpret_cast<const uint4 *>(box + (i * 8 + lane / 4) * 64 + piece * 2);
+                            if (c + i * 8 + lane / 4 < tokens && n + piece < p.N) *reinterpret_cast<uint4 *>(dst) = x;
+                            dst += step;
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
                 }
+                release();
                 continue;
             }
             const int rows = min(tl.row_end, tl.row0 + pair_rank * kTileX + kRows) - (tl.row0 + wrow);   // of the warp's 32
