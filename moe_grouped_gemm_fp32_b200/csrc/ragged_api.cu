@@ -133,14 +133,18 @@ dg_status_t m_grouped(const void *a, const void *b, void *d, const int32_t *offs
     if (T == 0) return DG_SUCCESS;
     const dg::RaggedParams p = ragged_params(d, offsets, T, 0, N, K, G, 0, info);
     // 256-row CTA pairs where an expert has 128 rows or more on average and there are a
-    // few of their tiles: 8 experts of 256 rows, 1024 x 1024: 32 pair tiles 13.4 us, 128
-    // single ones 17.0; one expert of 512 rows: 8 pair tiles 10.9 us, 64 single ones 8.5.
-    // Thin tiles of 32 rows where experts have 16 or fewer on average (19 rows, 520 x
-    // 2048: 12.9 us in tiles of 128 rows, 18.6 in thin ones, of which some experts then
-    // need several).  Tiles 64 wide where 128 would leave SMs without one.
+    // few of their tiles: 8 experts of 128 rows, 2048 x 4096: 32.8 us in pair tiles, 50.3 in
+    // single ones; one expert of 512 rows, 1024 x 1024: 8 pair tiles 10.5 us, 64 single
+    // ones 8.5.  Thin tiles of 32 rows where experts have 24 or fewer on average, so that
+    // few need several (16 experts of 4096 x 7168, tiles of 128 rows against thin ones: 24
+    // rows on average, skewed, 154 and 145 us, 48 rows 157 and 169), or where the thin ones
+    // fill no more than the SMs once: a call of few tiles takes as long as one tile does
+    // (one expert of 256 rows, 1024 x 8192, 128 thin tiles: 32.4 and 18.6; 192 rows, 4096 x
+    // 4096, 384 of them: 19.8 and 26.2).  Tiles 64 wide where 128 would leave SMs without one
+    // (one expert of 16 rows, 4096 x 7168: 16.8 us, 22.7 in the wider ones).
     const long long pair_tiles = ceil_div(T, 256) * ceil_div(N, 256);
     const bool pair = N > 128 && T / used >= 128 && 8 * pair_tiles >= info->num_sms;
-    const bool thin = !pair && T / used <= 16;
+    const bool thin = !pair && (T / used <= 24 || ceil_div(T, 32) * ceil_div(N, 64) <= info->num_sms);
     const int rows = pair ? 256 : thin ? 32 : 128;
     const long long filled = ceil_div(T, rows) > used ? ceil_div(T, rows) : used;     // row blocks, about
     const int bn = pair ? 256 : ceil_div(N, 128) * filled >= info->num_sms ? 128 : 64;

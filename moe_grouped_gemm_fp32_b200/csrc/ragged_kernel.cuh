@@ -30,7 +30,8 @@
 // Output.  A lane holds one row of the accumulator; stored straight from there,
 // each instruction touches 32 lines (weight gradient of 64 experts, 62 tokens each,
 // 1000 x 2112, BF16: 174 us, against 46 for its bytes).  So a warp turns 32 x 32
-// boxes around in shared memory and stores runs of a row.
+// boxes (single CTAs of kNT, kNN: 32 weights x 16 tokens) around in shared memory and
+// stores runs of a row.
 //
 // Roles: warp 0 producer (TMA), warp 1 TMEM and MMA issue, warp 2 clears ragged
 // token rows (kTN), warps 4.. epilogue: warp w drains TMEM lanes 32 (w % 4), columns
@@ -42,7 +43,7 @@
 // A and half of B's columns.  Single CTAs take over where experts have few
 // rows: there A comes in boxes of 32 rows, only those that the expert has, so
 // that weight bytes, not token tiles, fill the memory pipeline.  Where experts have
-// a few rows, tiles are thin (kRows 32): a stage keeps 4 KB for A and not 16, and
+// a few rows, or the call few tiles, they are thin (kRows 32): a stage keeps 4 KB for A and not 16, and
 // twice as many weight bytes are in flight (64 rows over 16 experts, 4096 x 7168: 156
 // -> 143 us, 98 % of the copy rate).
 //
@@ -55,8 +56,8 @@
 //
 // Precision.  The tensor core's FP32 accumulator truncates: measured against 64
 // bits, a sum of 8192 products loses 9e-6 (relative, 2-norm) and 32768 products
-// 1.9e-5, where rounded FP32 sums lose 1e-6 and 2.3e-6.  A BF16 result rounds
-// at 2^-9 and does not see it.  An FP32 weight gradient does, so it is summed
+// 1.9e-5, where rounded FP32 sums lose 1e-6 and 2.3e-6.  A BF16 result is rounded
+// by up to 2^-8 of itself and does not see it.  An FP32 weight gradient does, so it is summed
 // in two levels: every kSegBlocks K-blocks (512 tokens, 5e-7) the accumulator
 // is read out and added, rounded, to FP32 registers of the epilogue warps.
 //
@@ -100,7 +101,7 @@ struct RaggedSmem {
     static constexpr int kBBytes = kBCols * 128;
     // K-blocks of 64 in a stage: two in thin tiles of 64 columns, where few tiles wait on
     // a block's barriers and issue (0.2 us) rather than on its bytes: 4 rows, 1024 x
-    // 8192, 27.3 -> 21.9 us
+    // 8192, 26.2 -> 17.6 us; four a stage, of which then three fit: 19.7
     static constexpr int kSub = kRows == 32 && kBN == 64 ? 2 : 1;
     static constexpr int kSubBytes = kABytes + kBBytes;
     static constexpr int kStageBytes = kSub * kSubBytes;
