@@ -43,9 +43,9 @@
 // A and half of B's columns.  Single CTAs take over where experts have few
 // rows: there A comes in boxes of 32 rows, only those that the expert has, so
 // that weight bytes, not token tiles, fill the memory pipeline.  Where experts have
-// a few rows, or the call few tiles, they are thin (kRows 32): a stage keeps 4 KB for A and not 16, and
-// twice as many weight bytes are in flight (64 rows over 16 experts, 4096 x 7168: 156
-// -> 143 us, 98 % of the copy rate).
+// a few rows, or the call few tiles, they are thin (kRows 32): a stage keeps 4 KB for
+// A and not 16, and twice as many weight bytes are in flight (64 rows over 16 experts,
+// 4096 x 7168: 156 -> 143 us, 98 % of the copy rate).
 //
 // Single CTAs of kNT and kNN make the weights the MMA's 128 rows and the tokens its
 // columns, as many as the expert has, rounded up to 16: the other way round, products
@@ -57,8 +57,8 @@
 // Precision.  The tensor core's FP32 accumulator truncates: measured against 64
 // bits, a sum of 8192 products loses 9e-6 (relative, 2-norm) and 32768 products
 // 1.9e-5, where rounded FP32 sums lose 1e-6 and 2.3e-6.  A BF16 result is rounded
-// by up to 2^-8 of itself and does not see it.  An FP32 weight gradient does, so it is summed
-// in two levels: every kSegBlocks K-blocks (512 tokens, 5e-7) the accumulator
+// by up to 2^-8 of itself and does not see it.  An FP32 weight gradient does, so it is
+// summed in two levels: every kSegBlocks K-blocks (512 tokens, 5e-7) the accumulator
 // is read out and added, rounded, to FP32 registers of the epilogue warps.
 //
 // Every wait is bounded (BoundedWait).

@@ -155,6 +155,17 @@ K_SIZES = [
 ]
 
 
+# few tiles of one expert in several row blocks; 128 rows by 64 and by 128 columns; 24
+# rows on average by 128 columns, some experts with several row blocks or none
+@pytest.mark.parametrize("ints", [True, False])
+@pytest.mark.parametrize("sizes,lead,trail", [([256], 0, 0), ([257], 5, 40), ([33, 0, 95], 1, 2), ([100, 90, 129, 81], 3, 7),
+                                              ([100] * 19 + [127], 0, 9), ([0, 20, 64, 31, 1, 33] * 4, 2, 30)])
+@pytest.mark.parametrize("direction", [NT, NN])
+def test_m_grouped_on_single_ctas(direction, sizes, lead, trail, ints):
+    c = Case(direction, sizes, 1032, 1064, lead, trail, ints)
+    c.check(c.run(), ints)
+
+
 @pytest.mark.parametrize("ints", [True, False])
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("p,q", [(8, 8), (136, 264), (520, 1000), (264, 72)])
