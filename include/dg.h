@@ -275,7 +275,8 @@ DG_API dg_status_t dg_m_grouped_bf16_gemm_nt_masked(const void *a, const void *b
  *             written.  Offsets out of order or range are recorded as
  *             DG_ERR_INVALID_VALUE in the device status word; the kernel then
  *             uses them clamped to [0, M_total] and raised to the largest before.
- * Sums are FP32, d is BF16 (RNE).  M_total >= 0; K, N > 0 and multiples of 8;
+ * Sums are FP32 (runs of 1024 products on the tensor core, which truncates, added
+ * with rounding), d is BF16 (RNE).  M_total >= 0; K, N > 0 and multiples of 8;
  * 1 <= G <= 1024.  a and d may be NULL when M_total == 0 (a no-op).  M_total above
  * 2^31 - 1025 and sizes whose number of 32 x 64 tiles passes 2^31 - 1 are
  * DG_ERR_UNSUPPORTED_SHAPE.
@@ -307,10 +308,12 @@ DG_API dg_status_t dg_m_grouped_bf16_gemm_nn_ragged(const void *a, const void *b
  * of the earlier ones; BF16: added in FP32, rounded once).
  * k_offsets as m_offsets above, over K_total; tokens outside [k_offsets[0],
  * k_offsets[G]) reach no result, whatever they hold.
- * FP32 results are summed in FP32 with rounding (the tensor core's own sums,
- * which truncate, run over 512 tokens at a time).  M, N > 0 and multiples of 8;
- * 1 <= G <= 1024; K_total up to 2^31 - 1025 and G * M * N / 2^14 below 2^31.  K_total == 0 writes zeros (accumulate: a no-op); a and b may
- * then be NULL.  Results do not depend on the order of execution.
+ * Sums are FP32: the tensor core's own, which truncate, run over 512 tokens at a
+ * time (d BF16: 1024, or all of a call of up to 8192, where truncation costs
+ * about 4.7e-5 of a sum of one sign) and are added with rounding.  M, N > 0 and
+ * multiples of 8; 1 <= G <= 1024; K_total up to 2^31 - 1025 and G * M * N / 2^14
+ * below 2^31.  K_total == 0 writes zeros (accumulate: a no-op); a and b may then be
+ * NULL.  Results do not depend on the order of execution.
  */
 DG_API dg_status_t dg_k_grouped_bf16_gemm_tn_ragged(const void *a, const void *b, void *d,
                                                     int d_is_fp32, const int32_t *k_offsets, int G,

@@ -36,8 +36,8 @@
 // Roles: warp 0 producer (TMA), warp 1 TMEM and MMA issue, warp 2 clears ragged
 // token rows (kTN), warps 4.. epilogue: warp w drains TMEM lanes 32 (w % 4), columns
 // of half (w / 4 - 1) % 2.  Persistent; two accumulators in rotation, so the next
-// tile's MMAs overlap this tile's stores, and a group of 8 epilogue warps for each,
-// so that short tiles (few tokens, kTN; short K) store two at a time.
+// tile's MMAs overlap this tile's stores; with one-level sums a group of 8 epilogue
+// warps for each, so that tiles of few tokens store two at a time.
 //
 // CTA pairs (kCtaGroup == 2): 256 x kBN tiles, each CTA stages its 128 rows of
 // A and half of B's columns.  Single CTAs take over where experts have few
@@ -56,10 +56,16 @@
 //
 // Precision.  The tensor core's FP32 accumulator truncates: measured against 64
 // bits, a sum of 8192 products loses 9e-6 (relative, 2-norm) and 32768 products
-// 1.9e-5, where rounded FP32 sums lose 1e-6 and 2.3e-6.  A BF16 result is rounded
-// by up to 2^-8 of itself and does not see it.  An FP32 weight gradient does, so it is
-// summed in two levels: every kSegBlocks K-blocks (512 tokens, 5e-7) the accumulator
-// is read out and added, rounded, to FP32 registers of the epilogue warps.
+// 1.9e-5, where rounded FP32 sums lose 1e-6 and 2.3e-6; products of one sign lose in
+// proportion to their number (16.8 million of them: 9.7 %).  So sums have two
+// levels: every kSegBlocks K-blocks the accumulator is read out and added, rounded, to
+// FP32 registers of the epilogue warps.  A segment is 512 products for FP32 results
+// (5e-7) and 1024 for BF16 ones (1e-6): each costs the tensor core a pause of 0.2 us,
+// seen where one tile's latency is the call's (one expert of 64 rows, 512 x 8192:
+// 17.2 us in one level, 20.4 with 512, 18.8 with 1024, 17.9 with 2048) and not
+// elsewhere (64 rows, 16 experts, 4096 x 7168: 137 each; 64 experts of 62 rows, 1000 x
+// 2112: 59.0 and 59.9).  Only short BF16 weight gradients go without (rule and figures in
+// ragged_api.cu).
 //
 // Every wait is bounded (BoundedWait).
 #pragma once
@@ -72,14 +78,13 @@ namespace dg {
 enum RaggedDir : int { kNT = 0, kNN = 1, kTN = 2 };
 
 // 4 warps that load, multiply and clear rows, and 8 warps for each accumulator in
-// rotation; two-level FP32 sums take one such group, with more registers
-__host__ __device__ constexpr int ragged_threads(bool f32) { return f32 ? 384 : 640; }
+// rotation; two-level sums take one such group, with more registers
+__host__ __device__ constexpr int ragged_threads(bool two_level) { return two_level ? 384 : 640; }
 constexpr int kRaggedBlockK = 64;
 // Row blocks per L2 raster band at most; an expert's bands are equally high (33 row
 // blocks of 8192 tokens and a few: 11 each).  Bands of 8, 12, 16, 32 on the prompt's
 // input gradient: 1413, 1359, 1369, 1496 us.
 constexpr int kRaggedBand = 16;
-constexpr int kSegBlocks = 8;         // K-blocks per accumulator segment, FP32 weight gradient
 constexpr unsigned kSiteBadOffsets = 12, kSiteTailRows = 13;
 
 struct RaggedParams {
@@ -94,7 +99,7 @@ struct RaggedParams {
     int debug_flags;
 };
 
-template <int kDir, int kBN, int kStages, int kCtaGroup, bool kF32, int kRows>
+template <int kDir, int kBN, int kStages, int kCtaGroup, bool kF32, int kRows, bool kTwoLevel>
 struct RaggedSmem {
     static constexpr int kABytes = kRows * 128;
     static constexpr int kBCols = kBN / kCtaGroup;            // this CTA's columns of B
@@ -114,7 +119,7 @@ struct RaggedSmem {
     // epilogue: 32 rows by 32 columns for each of its warps
     static constexpr int kBoxBytes = 32 * 32 * (kF32 ? 4 : 2);
     static constexpr int kOutOffset = (kPrefixOffset + (kMaxGroups + 1) * 4 + 1023) / 1024 * 1024;
-    static constexpr int kUsed = kOutOffset + (ragged_threads(kF32) / 32 - 4) * kBoxBytes;
+    static constexpr int kUsed = kOutOffset + (ragged_threads(kTwoLevel) / 32 - 4) * kBoxBytes;
     static constexpr int kAlloc = (kUsed + 1024 > kMinSmem) ? kUsed + 1024 : kMinSmem;
     static constexpr bool kSwap = kDir != kTN && kCtaGroup == 1;     // weights are rows, tokens columns
     static constexpr int kAccCols = kSwap ? kRows : kBN;
@@ -327,13 +332,14 @@ struct BoxWriter {
 
 // tm_a, tm_b: see the operand table above (kNT, kNN single-CTA: A boxes of 32 rows).
 // kRows: rows of a CTA's tile (32 or 128).
-template <int kDir, int kBN, int kStages, int kCtaGroup, bool kF32, int kRows>
-__global__ void __launch_bounds__(ragged_threads(kF32), 1)
+template <int kDir, int kBN, int kStages, int kCtaGroup, bool kF32, int kRows, bool kTwoLevel>
+__global__ void __launch_bounds__(ragged_threads(kTwoLevel), 1)
 ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                    const RaggedParams p) {
-    using L = RaggedSmem<kDir, kBN, kStages, kCtaGroup, kF32, kRows>;
+    using L = RaggedSmem<kDir, kBN, kStages, kCtaGroup, kF32, kRows, kTwoLevel>;
     using Tile = RaggedTile<kDir, kBN, kCtaGroup, kRows>;
     static_assert(!kF32 || kDir == kTN, "FP32 output: weight gradient");
+    static_assert(kTwoLevel || (kDir == kTN && !kF32), "one-level sums: short BF16 weight gradients");
     static_assert(kRows == kTileX || (kRows == 32 && kDir != kTN && kCtaGroup == 1), "thin tiles: one CTA, K-major A");
     constexpr bool kSwap = L::kSwap;
     // the weight descriptor of a tile of 64 runs on over as many rows that follow
@@ -343,8 +349,9 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
     constexpr int kAccBufs = L::kAccBufs;
     constexpr int kEpiWarp0 = 4;
     constexpr int kHalf = kBN / 2;                 // columns per epilogue warp
-    constexpr bool kPromote = kF32;                // two-level sums
-    constexpr bool kRebalance = kPromote && kHalf >= 128;
+    constexpr bool kRebalance = kTwoLevel && !kSwap && kHalf >= 128;   // see kRegsLaunch
+    constexpr int kSegBlocks = kF32 ? 8 : 16;      // K-blocks per accumulator segment of two-level sums
+    static_assert(kSegBlocks % L::kSub == 0, "a segment is whole stages");
 
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -569,7 +576,7 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
                                                  : ragged_idesc(kTileX * kCtaGroup, kBN, kAMn, kBMn);
                     // one accumulator for the tile (nothing in it for an expert without tokens), or
                     // one for each segment
-                    const int seg = kPromote ? kSegBlocks : max(tl.num_kb, 1);
+                    const int seg = kTwoLevel ? kSegBlocks : max(tl.num_kb, 1);
                     for (int kb0 = 0; ok && kb0 < max(tl.num_kb, 1); kb0 += seg) {
                         if (!wait(tempty_bar(buf), tphase ^ 1u, kSiteMmaTmemEmpty)) { ok = false; break; }
                         ptx::tc_fence_after();
@@ -664,35 +671,53 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
                 if (kPair && !mma_cta) ptx::mbar_arrive_remote(leader_addr(tempty_bar(buf)));
                 else ptx::mbar_arrive(tempty_bar(buf));
             }
-            if (kPromote) buf ^= 1;
-            if (!kPromote || buf == 0) tphase ^= 1u;
+            if (kTwoLevel) buf ^= 1;
+            if (!kTwoLevel || buf == 0) tphase ^= 1u;
         };
         Tile tl;
-        const int e_step = kPromote ? t_step : 2 * t_step;
+        const int e_step = kTwoLevel ? t_step : 2 * t_step;
         for (int t = t_first + group * t_step; ok && t < num_tiles; t += e_step) {
             tl.decode(t, p, offs, prefix);
             if constexpr (kSwap) {
                 // lanes are weights, columns tokens: a warp turns 32 weights by 16 tokens round
-                if (!wait(tfull_bar(buf), tphase, kSitePromoFull)) { ok = false; break; }
-                ptx::tc_fence_after();
                 const int first = half * (kRows / 2);                  // of the warp's tokens
                 const int tokens = min(tl.row_end - tl.row0 - first, kRows / 2);
                 const int n = tl.n0 + quarter * 32;
-                if (quarter * 32 < kBN && n < p.N) {
+                const bool mine = quarter * 32 < kBN && n < p.N;
+                float acc[kRows / 2];
+#pragma unroll
+                for (int j = 0; j < kRows / 2; ++j) acc[j] = 0.f;
+                for (int kb0 = 0; kb0 < tl.num_kb; kb0 += kSegBlocks) {
+                    if (!wait(tfull_bar(buf), tphase, kSitePromoFull)) { ok = false; break; }
+                    ptx::tc_fence_after();
+                    if (mine) {
+#pragma unroll
+                        for (int c = 0; c < kRows / 2; c += 16) {
+                            if (c < tokens) {
+                                float v[16];
+                                ptx::tmem_ld16(tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
+                                               static_cast<uint32_t>(buf * L::kAccCols + first + c), v);
+                                ptx::tmem_wait_ld();
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) acc[c + j] += v[j];
+                            }
+                        }
+                    }
+                    release();
+                }
+                if (!ok) break;
+                if (mine) {
                     uint8_t *box = smem + L::kOutOffset + (warp - kEpiWarp0) * L::kBoxBytes;
                     const int piece = lane % 4 * 8;
                     uint8_t *dst = static_cast<uint8_t *>(p.d) +
                                    (static_cast<size_t>(tl.row0 + first + lane / 4) * p.N + n + piece) * 2;
                     const size_t step = static_cast<size_t>(p.N) * 16;                 // 8 tokens
-#pragma unroll 1
-                    for (int c = 0; c < tokens; c += 16) {
-                        float v[16];
-                        ptx::tmem_ld16(tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
-                                       static_cast<uint32_t>(buf * L::kAccCols + first + c), v);
-                        ptx::tmem_wait_ld();
+#pragma unroll
+                    for (int c = 0; c < kRows / 2; c += 16) {
+                        if (c >= tokens) break;
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
-                            *reinterpret_cast<__nv_bfloat16 *>(box + j * 64 + lane * 2) = __float2bfloat16_rn(v[j]);
+                            *reinterpret_cast<__nv_bfloat16 *>(box + j * 64 + lane * 2) = __float2bfloat16_rn(acc[c + j]);
                         __syncwarp();
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
@@ -703,7 +728,6 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
                         __syncwarp();
                     }
                 }
-                release();
                 continue;
             }
             const int rows = min(tl.row_end, tl.row0 + pair_rank * kTileX + kRows) - (tl.row0 + wrow);   // of the warp's 32
@@ -722,7 +746,7 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
                 }
                 writer.put(c, v, p.N - c0 - c, add);
             };
-            if constexpr (kPromote) {
+            if constexpr (kTwoLevel) {
                 float acc[kHalf];
 #pragma unroll
                 for (int j = 0; j < kHalf; ++j) acc[j] = 0.f;
