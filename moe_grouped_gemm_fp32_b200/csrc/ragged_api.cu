@@ -84,7 +84,7 @@ struct Launch {
     }
 
     // tiles: an upper bound of the tile count
-    static dg_status_t run(const CUtensorMap &ma, const CUtensorMap &mb, const dg::RaggedParams &p, long long tiles,
+    static dg_status_t run(const dg::RaggedMaps<kDir> &maps, const dg::RaggedParams &p, long long tiles,
                            const DeviceInfo *info, cudaStream_t stream) {
         int units = 0;
         dg_status_t st = setup(info, &units);
@@ -96,7 +96,7 @@ struct Launch {
         cudaLaunchConfig_t cfg;
         cudaLaunchAttribute attr[2];
         config(cfg, attr, grid, stream);
-        cudaError_t e = cudaLaunchKernelEx(&cfg, kernel(), ma, mb, p);
+        cudaError_t e = cudaLaunchKernelEx(&cfg, kernel(), maps, p);
         return e == cudaSuccess ? DG_SUCCESS : cuda_fail(e, "ragged_gemm_kernel launch");
     }
 };
@@ -148,17 +148,17 @@ dg_status_t m_grouped(const void *a, const void *b, void *d, const int32_t *offs
     const int rows = pair ? 256 : thin ? 32 : 128;
     const long long filled = ceil_div(T, rows) > used ? ceil_div(T, rows) : used;     // row blocks, about
     const int bn = pair ? 256 : ceil_div(N, 128) * filled >= info->num_sms ? 128 : 64;
-    CUtensorMap ma, mb;
-    if ((st = make_kmajor_map(&ma, a, 2, K, T, 1, pair ? 128 : 32)) != DG_SUCCESS) return st;
-    st = kDir == dg::kNT ? make_kmajor_map(&mb, b, 2, K, N, G, pair ? bn / 2 : bn)
-                         : make_kmajor_map(&mb, b, 2, N, K, G, dg::kRaggedBlockK);
+    dg::RaggedMaps<kDir> maps;
+    if ((st = make_kmajor_map(&maps.a, a, 2, K, T, 1, pair ? 128 : 32)) != DG_SUCCESS) return st;
+    st = kDir == dg::kNT ? make_kmajor_map(&maps.b, b, 2, K, N, G, pair ? bn / 2 : bn)
+                         : make_kmajor_map(&maps.b, b, 2, N, K, G, dg::kRaggedBlockK);
     if (st != DG_SUCCESS) return st;
     const long long tiles = (ceil_div(T, rows) + used) * ceil_div(N, bn);
-    if (pair) return Launch<kDir, 256, 5, 2, false>::run(ma, mb, p, tiles, info, stream);
-    if (thin && bn == 128) return Launch<kDir, 128, 9, 1, false, 32>::run(ma, mb, p, tiles, info, stream);
-    if (thin) return Launch<kDir, 64, 7, 1, false, 32>::run(ma, mb, p, tiles, info, stream);
-    if (bn == 128) return Launch<kDir, 128, 5, 1, false>::run(ma, mb, p, tiles, info, stream);
-    return Launch<kDir, 64, 7, 1, false>::run(ma, mb, p, tiles, info, stream);
+    if (pair) return Launch<kDir, 256, 5, 2, false>::run(maps, p, tiles, info, stream);
+    if (thin && bn == 128) return Launch<kDir, 128, 9, 1, false, 32>::run(maps, p, tiles, info, stream);
+    if (thin) return Launch<kDir, 64, 7, 1, false, 32>::run(maps, p, tiles, info, stream);
+    if (bn == 128) return Launch<kDir, 128, 5, 1, false>::run(maps, p, tiles, info, stream);
+    return Launch<kDir, 64, 7, 1, false>::run(maps, p, tiles, info, stream);
 }
 
 // Most tokens of a call whose BF16 weight gradient is summed in one level.  What the
@@ -171,15 +171,20 @@ constexpr int kOneLevelTokens = 8192;
 template <bool kF32, bool kTwoLevel>
 dg_status_t k_grouped(const void *a, const void *b, const dg::RaggedParams &p, const DeviceInfo *info,
                       cudaStream_t stream) {
-    CUtensorMap ma, mb;
-    dg_status_t st = make_kmajor_map(&ma, a, 2, p.M, p.T, 1, dg::kRaggedBlockK);
+    dg::RaggedMaps<dg::kTN> maps;
+    dg_status_t st = DG_SUCCESS;
+    auto encode = [&](CUtensorMap *ma, CUtensorMap *mb, int tokens) {
+        if (st == DG_SUCCESS) st = make_kmajor_map(ma, a, 2, p.M, p.T, 1, tokens);
+        if (st == DG_SUCCESS) st = make_kmajor_map(mb, b, 2, p.N, p.T, 1, tokens);
+    };
+    encode(&maps.a, &maps.b, dg::kRaggedBlockK);
+    for (int i = 0; i < dg::kTailMaps; ++i) encode(&maps.a_tail[i], &maps.b_tail[i], dg::tail_rows(i));
     if (st != DG_SUCCESS) return st;
-    if ((st = make_kmajor_map(&mb, b, 2, p.N, p.T, 1, dg::kRaggedBlockK)) != DG_SUCCESS) return st;
     if (p.M > 128 && p.N > 128)
         return Launch<dg::kTN, 256, 5, 2, kF32, 128, kTwoLevel>::run(
-            ma, mb, p, p.G * ceil_div(p.M, 256) * ceil_div(p.N, 256), info, stream);
+            maps, p, p.G * ceil_div(p.M, 256) * ceil_div(p.N, 256), info, stream);
     return Launch<dg::kTN, 128, 5, 1, kF32, 128, kTwoLevel>::run(
-        ma, mb, p, p.G * ceil_div(p.M, 128) * ceil_div(p.N, 128), info, stream);
+        maps, p, p.G * ceil_div(p.M, 128) * ceil_div(p.N, 128), info, stream);
 }
 
 }  // namespace

@@ -20,12 +20,16 @@
 //     computed from the neighbour's tokens and not stored.  Rows of the product
 //     do not mix, so a NaN there stays there.
 //   kTN: the last block of 64 tokens of an expert may run into the next one's.
-//     Its MMAs stop at the last started group of 16 tokens, and the rows
-//     between the expert's end and that group's end are zeroed in shared
-//     memory, in both operands (0 * NaN would be NaN), by a warp of its own:
-//     the block's loads complete on a barrier of that warp, which clears the
-//     rows and only then hands the stage to the MMA warp.  The block comes last,
-//     so the MMAs of the blocks before it run meanwhile.
+//     Its MMAs stop at the last started group of 16 tokens, and the rows between
+//     the expert's end and that group's end have to be zeros, in both operands (0 *
+//     NaN would be NaN).  They come by TMA like the tokens themselves: such a block is
+//     put together from boxes of tail_rows(i) tokens, and for the zeros from boxes
+//     that lie behind the buffer's last row.  So whatever the MMAs read, the
+//     second CTA of a pair included, has arrived on the one barrier that they wait
+//     for.  (Rows that a warp clears by plain stores have to be released to the other
+//     CTA's tensor core at cluster scope: weight gradient of 64 experts of 62 tokens,
+//     1000 x 2112, BF16, 80.6 us against 70.3.  Boxes of 32, 16, 8, 4, 2 and 1 tokens:
+//     70.4, and 1 us more on the host for their maps.)
 //
 // Output.  A lane holds one row of the accumulator; stored straight from there,
 // each instruction touches 32 lines (weight gradient of 64 experts, 62 tokens each,
@@ -33,8 +37,7 @@
 // boxes (single CTAs of kNT, kNN: 32 weights x 16 tokens) around in shared memory and
 // stores runs of a row.
 //
-// Roles: warp 0 producer (TMA), warp 1 TMEM and MMA issue, warp 2 clears ragged
-// token rows (kTN), warps 4.. epilogue: warp w drains TMEM lanes 32 (w % 4), columns
+// Roles: warp 0 producer (TMA), warp 1 TMEM and MMA issue, warps 4.. epilogue: warp w drains TMEM lanes 32 (w % 4), columns
 // of half (w / 4 - 1) % 2.  Persistent; two accumulators in rotation, so the next
 // tile's MMAs overlap this tile's stores; with one-level sums a group of 8 epilogue
 // warps for each, so that tiles of few tokens store two at a time.
@@ -77,15 +80,17 @@ namespace dg {
 
 enum RaggedDir : int { kNT = 0, kNN = 1, kTN = 2 };
 
-// 4 warps that load, multiply and clear rows, and 8 warps for each accumulator in
-// rotation; two-level sums take one such group, with more registers
+// 4 warps that load and multiply, and 8 warps for each accumulator in rotation; two-level sums take one such group, with more registers
 __host__ __device__ constexpr int ragged_threads(bool two_level) { return two_level ? 384 : 640; }
 constexpr int kRaggedBlockK = 64;
 // Row blocks per L2 raster band at most; an expert's bands are equally high (33 row
 // blocks of 8192 tokens and a few: 11 each).  Bands of 8, 12, 16, 32 on the prompt's
 // input gradient: 1413, 1359, 1369, 1496 us.
 constexpr int kRaggedBand = 16;
-constexpr unsigned kSiteBadOffsets = 12, kSiteTailRows = 13;
+constexpr unsigned kSiteBadOffsets = 12;
+// kTN: tokens of the boxes that an expert's last block is put together from
+constexpr int kTailMaps = 3;
+__host__ __device__ constexpr int tail_rows(int i) { return i == 0 ? 16 : i == 1 ? 4 : 1; }
 
 struct RaggedParams {
     void *d;
@@ -97,6 +102,17 @@ struct RaggedParams {
     int G;
     int accumulate;           // kTN: add to d
     int debug_flags;
+};
+
+// The operands' tensor maps; kNT, kNN single CTAs: A boxes of 32 rows.
+template <int kDir>
+struct RaggedMaps {
+    CUtensorMap a, b;
+};
+template <>
+struct RaggedMaps<kTN> {
+    CUtensorMap a, b;                                 // boxes of kRaggedBlockK tokens
+    CUtensorMap a_tail[kTailMaps], b_tail[kTailMaps]; // of tail_rows(i)
 };
 
 template <int kDir, int kBN, int kStages, int kCtaGroup, bool kF32, int kRows, bool kTwoLevel>
@@ -112,7 +128,7 @@ struct RaggedSmem {
     static constexpr int kStageBytes = kSub * kSubBytes;
     static constexpr int kAccBufs = 2;
     static constexpr int kBarOffset = kStages * kStageBytes;
-    static constexpr int kNumBars = 3 * kStages + 2 * kAccBufs + 1;
+    static constexpr int kNumBars = 2 * kStages + 2 * kAccBufs + 1;
     static constexpr int kMiscOffset = kBarOffset + kNumBars * 8;   // tmem addr, abort flag
     static constexpr int kOffsOffset = (kMiscOffset + 16 + 15) / 16 * 16;
     static constexpr int kPrefixOffset = kOffsOffset + (kMaxGroups + 1) * 4;
@@ -330,12 +346,10 @@ struct BoxWriter {
     }
 };
 
-// tm_a, tm_b: see the operand table above (kNT, kNN single-CTA: A boxes of 32 rows).
 // kRows: rows of a CTA's tile (32 or 128).
 template <int kDir, int kBN, int kStages, int kCtaGroup, bool kF32, int kRows, bool kTwoLevel>
 __global__ void __launch_bounds__(ragged_threads(kTwoLevel), 1)
-ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
-                   const RaggedParams p) {
+ragged_gemm_kernel(const __grid_constant__ RaggedMaps<kDir> maps, const RaggedParams p) {
     using L = RaggedSmem<kDir, kBN, kStages, kCtaGroup, kF32, kRows, kTwoLevel>;
     using Tile = RaggedTile<kDir, kBN, kCtaGroup, kRows>;
     static_assert(!kF32 || kDir == kTN, "FP32 output: weight gradient");
@@ -360,10 +374,9 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
     const uint32_t bar_base = s_base + L::kBarOffset;
     auto full_bar = [&](int s) { return bar_base + 8u * s; };
     auto empty_bar = [&](int s) { return bar_base + 8u * (kStages + s); };
-    auto tail_bar = [&](int s) { return bar_base + 8u * (2 * kStages + s); };
-    auto tfull_bar = [&](int b) { return bar_base + 8u * (3 * kStages + b); };
-    auto tempty_bar = [&](int b) { return bar_base + 8u * (3 * kStages + kAccBufs + b); };
-    const uint32_t mma_done_bar = bar_base + 8u * (3 * kStages + 2 * kAccBufs);
+    auto tfull_bar = [&](int b) { return bar_base + 8u * (2 * kStages + b); };
+    auto tempty_bar = [&](int b) { return bar_base + 8u * (2 * kStages + kAccBufs + b); };
+    const uint32_t mma_done_bar = bar_base + 8u * (2 * kStages + 2 * kAccBufs);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kMiscOffset);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kMiscOffset + 4);
     int *offs = reinterpret_cast<int *>(smem + L::kOffsOffset);
@@ -377,13 +390,11 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
     auto leader_addr = [&](uint32_t local) { return kPair ? ptx::map_cluster(local, 0) : local; };
 
     if (threadIdx.x == 0) {
-        ptx::prefetch_tmap(&tm_a);
-        ptx::prefetch_tmap(&tm_b);
+        ptx::prefetch_tmap(&maps.a);
+        ptx::prefetch_tmap(&maps.b);
         for (int i = 0; i < kStages; ++i) {
-            // kTN: one arrival per CTA (its producer, or its row-clearing warp)
-            ptx::mbar_init(full_bar(i), kDir == kTN ? kCtaGroup : 1);
+            ptx::mbar_init(full_bar(i), 1);
             ptx::mbar_init(empty_bar(i), 1);
-            ptx::mbar_init(tail_bar(i), 1);
         }
         for (int b = 0; b < kAccBufs; ++b) {
             ptx::mbar_init(tfull_bar(b), 1);
@@ -392,6 +403,12 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
         ptx::mbar_init(mma_done_bar, 1);
         *abort_flag = 0;
         ptx::fence_mbar_init();
+    }
+    if constexpr (kDir == kTN) {
+        if (warp == 2 && lane < kTailMaps) {
+            ptx::prefetch_tmap(&maps.a_tail[lane]);
+            ptx::prefetch_tmap(&maps.b_tail[lane]);
+        }
     }
     // The launch may overlap the end of the kernel before it in the stream: from here on
     // that kernel is done and its writes are visible.
@@ -474,7 +491,7 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
             // ======================================================== producer
             if (ptx::elect_one()) {
                 int stage = 0;
-                uint32_t phase = 0, tail_phase = 0, tail_armed = 0;   // a bit per stage
+                uint32_t phase = 0;
                 long long issued = 0;
                 bool ok = (p.debug_flags & kDebugProducerIdle) == 0;
                 Tile tl;
@@ -490,48 +507,54 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
                         const uint32_t sa = s_base + stage * L::kStageBytes;
                         const uint32_t sb = sa + L::kABytes;
                         const int k0 = kb * kRaggedBlockK;
-                        // the ragged last block of tokens goes through the row-clearing warp
-                        const bool clear = kDir == kTN && kb == tl.num_kb - 1 && (tl.tail & 15) != 0;
-                        uint32_t bar;
-                        if (clear) {
-                            bar = tail_bar(stage);
-                            ptx::mbar_arrive_expect_tx(bar, bytes);
-                            tail_armed |= 1u << stage;
-                            tail_phase ^= 1u << stage;
-                        } else if (kPair) {
-                            bar = leader_addr(full_bar(stage));
-                            if (mma_cta) ptx::mbar_arrive_expect_tx(full_bar(stage), 2u * bytes);
-                            else if (kDir == kTN) ptx::mbar_arrive_remote(bar);
-                        } else {
-                            bar = full_bar(stage);
-                            ptx::mbar_arrive_expect_tx(bar, bytes);
-                        }
+                        // an expert's last tokens, where they end inside a group of 16
+                        const bool ragged = kDir == kTN && kb == tl.num_kb - 1 && (tl.tail & 15) != 0;
+                        const uint32_t expect = ragged ? (tl.tail + 15) / 16 * 16 * ((2 + L::kBCols / 64) * 128u) : bytes;
+                        const uint32_t bar = leader_addr(full_bar(stage));
+                        if (mma_cta) ptx::mbar_arrive_expect_tx(full_bar(stage), kCtaGroup * expect);
                         auto load = [&](uint32_t dst, const CUtensorMap *m, int c0, int c1, int c2) {
-                            if (kPair && !clear) ptx::tma_load_3d_pair(dst, m, bar, c0, c1, c2);
+                            if constexpr (kPair) ptx::tma_load_3d_pair(dst, m, bar, c0, c1, c2);
                             else ptx::tma_load_3d(dst, m, bar, c0, c1, c2);
                         };
                         if constexpr (kDir == kTN) {
+                            // rows of all boxes from `row` on, the tokens from `tok` on
+                            auto load_rows = [&](const CUtensorMap *a, const CUtensorMap *b, int row, int tok) {
+                                for (int i = 0; i < 2; ++i)
+                                    load(sa + i * 8192u + row * 128u, a, tl.row0 + pair_rank * kTileX + 64 * i, tok, 0);
+                                for (int i = 0; i < L::kBCols / 64; ++i)
+                                    load(sb + i * 8192u + row * 128u, b, nb0 + 64 * i, tok, 0);
+                            };
                             const int tok = tl.tok0 + k0;
-                            for (int i = 0; i < 2; ++i)
-                                load(sa + i * 8192u, &tm_a, tl.row0 + pair_rank * kTileX + 64 * i, tok, 0);
-                            for (int i = 0; i < L::kBCols / 64; ++i)
-                                load(sb + i * 8192u, &tm_b, nb0 + 64 * i, tok, 0);
+                            if (!ragged) {
+                                load_rows(&maps.a, &maps.b, 0, tok);
+                            } else {
+                                int row = 0;
+#pragma unroll
+                                for (int i = 0; i < kTailMaps; ++i)
+                                    for (; row + tail_rows(i) <= tl.tail; row += tail_rows(i))
+                                        load_rows(&maps.a_tail[i], &maps.b_tail[i], row, tok + row);
+                                const int end = (tl.tail + 15) / 16 * 16;
+#pragma unroll
+                                for (int i = 1; i < kTailMaps; ++i)                  // zeros: behind the last token
+                                    for (; row + tail_rows(i) <= end; row += tail_rows(i))
+                                        load_rows(&maps.a_tail[i], &maps.b_tail[i], row, p.T);
+                            }
                         } else {
 #pragma unroll
                             for (int s = 0; s < L::kSub; ++s) {          // (past K: zeros)
                                 const uint32_t a = sa + s * L::kSubBytes, b = a + L::kABytes;
                                 const int k = k0 + s * kRaggedBlockK;
                                 if constexpr (kPair) {
-                                    load(a, &tm_a, k, tl.row0 + pair_rank * kTileX, 0);
+                                    load(a, &maps.a, k, tl.row0 + pair_rank * kTileX, 0);
                                 } else {
                                     for (int i = 0; i < a_boxes; ++i)
-                                        load(a + i * 4096u, &tm_a, k, tl.row0 + 32 * i, 0);
+                                        load(a + i * 4096u, &maps.a, k, tl.row0 + 32 * i, 0);
                                 }
                                 if constexpr (kDir == kNT) {
-                                    load(b, &tm_b, k, nb0, tl.g);
+                                    load(b, &maps.b, k, nb0, tl.g);
                                 } else {
                                     for (int i = 0; i < L::kBCols / 64; ++i)
-                                        load(b + i * 8192u, &tm_b, nb0 + 64 * i, k, tl.g);
+                                        load(b + i * 8192u, &maps.b, nb0 + 64 * i, k, tl.g);
                                 }
                             }
                         }
@@ -539,9 +562,8 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
                         if (++stage == kStages) { stage = 0; phase ^= 1u; }
                     }
                 }
-                // never leave with TMA writes into shared memory in flight: the last
-                // blocks handed to the row-clearing warp, then the last stages.  A
-                // pair's second CTA cannot see its other bytes land; for it the final
+                // never leave with TMA writes into shared memory in flight.  A pair's
+                // second CTA cannot see its other bytes land; for it the final
                 // cluster barrier, reached after the MMA CTA consumed every stage (or
                 // ran out of time waiting for it), covers them.
                 auto drain = [&](uint32_t bar, uint32_t par) {
@@ -553,8 +575,6 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
                         }
                     }
                 };
-                for (int s = 0; s < kStages; ++s)
-                    if ((tail_armed >> s) & 1u) drain(tail_bar(s), ((tail_phase >> s) & 1u) ^ 1u);
                 const long long first = !mma_cta ? issued : (issued > kStages ? issued - kStages : 0);
                 for (long long i = first; i < issued; ++i)
                     drain(full_bar(static_cast<int>(i % kStages)), static_cast<uint32_t>((i / kStages) & 1));
@@ -617,38 +637,6 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
                 else ptx::mma_commit(mma_done_bar);
             }
             __syncwarp();
-        } else if (kDir == kTN && warp == 2) {
-            // ======================================================== clears ragged token rows
-            long long block = 0;                  // K-blocks of the tiles before
-            uint32_t tail_phase = 0;              // a bit per stage
-            Tile tl;
-            for (int t = t_first; t < num_tiles; t += t_step) {
-                tl.decode(t, p, offs, prefix);
-                block += tl.num_kb;
-                if (tl.num_kb == 0 || (tl.tail & 15) == 0) continue;
-                const int stage = static_cast<int>((block - 1) % kStages);
-                if (!wait(tail_bar(stage), (tail_phase >> stage) & 1u, kSiteTailRows)) break;
-                tail_phase ^= 1u << stage;
-                // rows tail .. next multiple of 16, one 128-byte line per box and row (the
-                // swizzle only permutes within a line)
-                const int rows = 16 - (tl.tail & 15);
-                constexpr int kBoxes = 2 + L::kBCols / 64;
-                uint8_t *base = smem + stage * L::kStageBytes + tl.tail * 128;
-                for (int i = lane; i < rows * 8; i += 32)
-#pragma unroll
-                    for (int box = 0; box < kBoxes; ++box)
-                        *reinterpret_cast<uint4 *>(base + box * 8192 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
-                // The MMAs read through the async proxy, each CTA's tensor core its own
-                // shared memory: the fence has the zeros there before the arrival leaves.
-                // (An arrival that also releases them at cluster scope waits for the
-                // epilogue's stores in flight as well, 2500 cycles a tile.)
-                ptx::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    if (kPair && !mma_cta) ptx::mbar_arrive_remote(leader_addr(full_bar(stage)));
-                    else ptx::mbar_arrive(full_bar(stage));
-                }
-            }
         }
     } else {
         // ============================================================ epilogue
