@@ -789,6 +789,10 @@ ragged_gemm_kernel(const __grid_constant__ RaggedMaps<kDir> maps, const RaggedPa
     pdl::grid_launch_dependents();
 
     // ---------------------------------------------------------------- teardown
+    ptx::tc_fence_before();
+    __syncthreads();
+    // (After the barrier: a pair's second CTA issues no MMAs, and would wait here from its
+    // start, so that the limit bounded the call.)
     if (warp == 1 && ptx::elect_one()) {
         const long long start = clock64();
         while (!ptx::mbar_try_wait(mma_done_bar, 0)) {
@@ -799,8 +803,6 @@ ragged_gemm_kernel(const __grid_constant__ RaggedMaps<kDir> maps, const RaggedPa
         }
     }
     __syncwarp();
-    ptx::tc_fence_before();
-    __syncthreads();
     if constexpr (kPair) ptx::cluster_sync_all();   // no CTA leaves while its peer may touch its smem
     if (warp == 1) {
         ptx::tc_fence_after();

@@ -85,7 +85,7 @@ ones = lambda *s: torch.ones(s, dtype=BF16, device="cuda")
 off = lambda n: torch.tensor([0, n], dtype=torch.int32, device="cuda")
 dg.dg_get_device_status(clear=True)
 L = 1 << 22
-for M, N in ((8, 16),):
+for M, N in ((8, 16), (136, 136)):
     for dtype in (F32, BF16):
         T = L + 5
         d = torch.zeros((1, M, N), dtype=dtype, device="cuda")
@@ -109,6 +109,16 @@ for name, f, w in (("forward", dg.dg_m_grouped_bf16_gemm_nt_ragged, ones(1, 8, L
     code = dg.dg_get_device_status(clear=True)
     print(name, "status %x" % code)
     assert code == 0 and bool((d == L).all())
+d = torch.zeros((2560, 264), dtype=BF16, device="cuda")
+x, w = ones(2560, L // 4), ones(264, L // 4)
+for name, f, w in (("forward, pairs", dg.dg_m_grouped_bf16_gemm_nt_ragged, w[None]),
+                   ("input gradient, pairs", dg.dg_m_grouped_bf16_gemm_nn_ragged, w.t().contiguous()[None])):
+    d.zero_()
+    f(x, w, d, off(2560))
+    torch.cuda.synchronize()
+    code = dg.dg_get_device_status(clear=True)
+    print(name, "status %x" % code)
+    assert code == 0 and bool((d == L // 4).all())
 print("OK")
 """
 
