@@ -11,7 +11,8 @@ namespace pdl {
 // All grids this one depends on have completed and their writes are visible.
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// The next grid may be scheduled once every block has called this (or ended).
+// The next grid may be scheduled once every block has called this (its first thread
+// that does so counts) or ended.
 __device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 }  // namespace pdl

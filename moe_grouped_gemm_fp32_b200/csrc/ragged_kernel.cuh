@@ -784,13 +784,16 @@ ragged_gemm_kernel(const __grid_constant__ RaggedMaps<kDir> maps, const RaggedPa
         }
     }
 
-    // The next grid's blocks may be placed: a block that comes earlier, on the SMs that
-    // are done first, would find the SMs unevenly filled.
-    pdl::grid_launch_dependents();
-
     // ---------------------------------------------------------------- teardown
     ptx::tc_fence_before();
     __syncthreads();
+    // The next grid's blocks may be placed.  The first thread of a block that says so
+    // counts, so none does before the block's tiles are done: blocks that come while some
+    // SMs are done fill the SMs unevenly (a 4-bit call of 8 tokens, 16384 x 7168, behind a
+    // forward of one expert of 16 rows, 1024 x 1024: 28.3 us for both with the signal at the
+    // end of each warp's own role, which idle warps reach at once, 25.1 here, 25.1 without
+    // it; that forward and its input gradient: 11.4, 11.6, 12.1).
+    if (threadIdx.x == 0) pdl::grid_launch_dependents();
     // (After the barrier: a pair's second CTA issues no MMAs, and would wait here from its
     // start, so that the limit bounded the call.)
     if (warp == 1 && ptx::elect_one()) {
