@@ -329,7 +329,9 @@ DG_API dg_status_t dg_k_grouped_bf16_gemm_tn_ragged(const void *a, const void *b
  *          and k + 1 in its high four
  *   scales [K/group_size, N] BF16 ("MN-major"): of row n and the group of
  *          group_size consecutive k
- *   zeros  [K/group_size, N] uint8, 0..127, or NULL for 8 everywhere
+ *   zeros  [K/group_size, N] uint8, 0..127, or NULL for 8 everywhere.  Larger ones
+ *          are recorded as DG_ERR_INVALID_VALUE in the device status word (their
+ *          low seven bits are used)
  * q - z is exact and the scale is applied to the group's FP32 sum, so no weight
  * is rounded.  group_size 32, 64 or 128, K % group_size == 0, N % 8 == 0,
  * N <= 65535 * 128.  Rows are taken 8, 16 or 32 at a time and the weights read

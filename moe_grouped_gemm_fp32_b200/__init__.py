@@ -491,8 +491,9 @@ def _w4_group_size(K, scales):
 def dg_w4_gemv_nt(x, w, scales, d, zeros=None, stream=None):
     """d [M,N] (bfloat16) = x [M,K] (bfloat16) times 4-bit weights: w uint8
     [N,K/2] (low four bits: even k), scales bfloat16 [K/group_size,N], zeros
-    uint8 of the scales' shape or None (8); weight = scale * (code - zero).  For
-    few rows.  w, scales and zeros may carry a leading dimension of 1."""
+    uint8, 0..127 (larger ones are recorded in the device status), of the scales'
+    shape or None (8); weight = scale * (code - zero).  For few rows.  w, scales
+    and zeros may carry a leading dimension of 1."""
     torch = _th()
     ptrs = (_req(x, torch.bfloat16, "x", 2), _req(w, torch.uint8, "w", (2, 3)),
             _req(scales, torch.bfloat16, "scales", (2, 3)), _req(d, torch.bfloat16, "d", 2))
@@ -512,8 +513,9 @@ def dg_w4_gemv_nt(x, w, scales, d, zeros=None, stream=None):
 
 def dg_m_grouped_w4_gemv_nt_ragged(x, w, scales, d, m_offsets, zeros=None, stream=None):
     """The 4-bit product grouped by expert over ragged rows: x [M_total,K], w
-    uint8 [G,N,K/2], scales bfloat16 [G,K/group_size,N], zeros uint8 of the
-    scales' shape or None, d [M_total,N]; m_offsets int32 [G+1] (device)."""
+    uint8 [G,N,K/2], scales bfloat16 [G,K/group_size,N], zeros uint8 (0..127, as
+    above) of the scales' shape or None, d [M_total,N]; m_offsets int32 [G+1]
+    (device)."""
     torch = _th()
     ptrs = (_req(x, torch.bfloat16, "x", 2), _req(w, torch.uint8, "w", 3),
             _req(scales, torch.bfloat16, "scales", 3), _req(d, torch.bfloat16, "d", 2),
