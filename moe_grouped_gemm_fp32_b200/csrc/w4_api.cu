@@ -68,6 +68,30 @@ dg_status_t launch_w4(dg::W4Params p, int split, int runs, cudaStream_t stream) 
     return e == cudaSuccess ? DG_SUCCESS : cuda_fail(e, "w4_gemv_kernel launch");
 }
 
+// CTAs that share a row block along K: the count with the least cost of the fullest SM,
+// in times that an SM with enough CTAs takes for a block of K.  It works through the blocks
+// of all of its CTAs; a wave of resident ones takes at least the latency of a CTA's blocks,
+// 2.5 such times each (2 with 16 or 32 tokens); and each CTA costs 3 to start and hand over.
+// Measured for 1 to 1000 row blocks, 4 to 128 blocks of K, 1 to 30 tokens (400 shapes, splits
+// of 1, 2, 4, 8): the choice takes 0.5 % more than the best one on average, 10 % at
+// worst.  512 row blocks of 55 K blocks, one token: 56.1 us whole, 50.1 halved.
+int k_split(long long row_blocks, int k_blocks, int tokens, int num_sms) {
+    const int resident = tokens <= 8 ? 5 : tokens <= 16 ? 4 : 3, latency = tokens <= 8 ? 5 : 4;    // in halves
+    int best = 1;
+    long long least = 0;
+    for (int split = 1; split <= 8 && (split == 1 || k_blocks >= 2 * split); split *= 2) {
+        const long long ctas = (row_blocks * split + num_sms - 1) / num_sms;
+        const long long waves = (ctas + resident - 1) / resident, blocks = (k_blocks + split - 1) / split;
+        const long long work = 2 * ctas * blocks, wait = waves * blocks * latency;
+        const long long cost = (work > wait ? work : wait) + 6 * ctas;
+        if (split == 1 || cost < least) {
+            least = cost;
+            best = split;
+        }
+    }
+    return best;
+}
+
 // runs of `rows` rows that M rows of `experts` experts can make at most
 int runs_of(int M, int experts, int rows) { return experts + (M - experts) / rows; }
 
@@ -108,16 +132,8 @@ dg_status_t w4_gemv(const void *x, const void *w, const void *s, const void *z, 
     // tokens a CTA takes at once: all (dense), or what an expert has on average and as much again
     const int experts = offsets ? (M < G ? M : G) : 0;
     const int tokens = M <= 8 || !experts ? M : 2 * ((M + experts - 1) / experts);
-    // K split: until there are two and a half CTAs for each SM, with 4 K blocks or more
-    // in each (fewer cost more in start-up than they save: 16 blocks over 56 row blocks
-    // 7.0 us split by 4, 7.4 by 8), and until no CTA has more than 55, so that the last
-    // ones to finish are short (56 blocks over 512 row blocks: 81 us whole, 70 halved).
     const long long blocks = static_cast<long long>((N + dg::kW4Rows - 1) / dg::kW4Rows) * (experts ? experts : 1);
-    const int kblocks = (K + dg::kW4BlockK - 1) / dg::kW4BlockK;
-    int split = 1;
-    while (split < 8 && kblocks / (2 * split) >= 4 &&
-           (blocks * split * 2 < 5LL * info->num_sms || kblocks / split > 55))
-        split *= 2;
+    const int split = k_split(blocks, (K + dg::kW4BlockK - 1) / dg::kW4BlockK, tokens, info->num_sms);
     if (group_size == 32) return dispatch<32>(p, tokens, experts, split, stream);
     if (group_size == 64) return dispatch<64>(p, tokens, experts, split, stream);
     return dispatch<128>(p, tokens, experts, split, stream);
