@@ -91,8 +91,8 @@ struct Launch {
         if (st != DG_SUCCESS) return st;
         const int grid = kCtaGroup * static_cast<int>(tiles < units ? tiles : units);
         if (verbose())
-            std::fprintf(stderr, "[dg] ragged dir=%d rows=%d bn=%d stages=%d ctas/mma=%d f32=%d grid=%d smem=%d\n", kDir,
-                         kRows, kBN, kStages, kCtaGroup, kF32 ? 1 : 0, grid, L::kAlloc);
+            std::fprintf(stderr, "[dg] ragged dir=%d rows=%d bn=%d stages=%d ctas/mma=%d f32=%d levels=%d grid=%d smem=%d\n",
+                         kDir, kRows, kBN, kStages, kCtaGroup, kF32 ? 1 : 0, kTwoLevel ? 2 : 1, grid, L::kAlloc);
         cudaLaunchConfig_t cfg;
         cudaLaunchAttribute attr[2];
         config(cfg, attr, grid, stream);

@@ -1,4 +1,4 @@
-"""GPU tests of the ragged and 4-bit products on several streams at once, each stream
+"""GPU tests of the ragged and 4-bit products on ten streams at once, each stream
 ordered behind the one that made its inputs and its result buffer."""
 import pytest
 import torch
