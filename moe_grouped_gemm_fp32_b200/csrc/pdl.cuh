@@ -3,6 +3,9 @@
 // on that kernel may be read, and nothing written, before grid_dependency_wait();
 // every block calls it, also one without work, so that a grid's end implies the
 // end of all before it.
+// Nor may what that kernel can have written be read as read-only data (__ldg, const
+// __restrict__): it changes while this kernel lives, and such reads may be moved before
+// the wait or served from a copy made before the write.
 #pragma once
 
 namespace dg {

@@ -422,7 +422,7 @@ ragged_gemm_kernel(const __grid_constant__ RaggedMaps<kDir> maps, const RaggedPa
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int i = base + 4 * lane + j;
-                raw[j] = i <= p.G ? __ldg(p.offsets + i) : 0;
+                raw[j] = i <= p.G ? p.offsets[i] : 0;
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {

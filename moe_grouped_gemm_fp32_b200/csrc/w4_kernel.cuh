@@ -174,7 +174,7 @@ __device__ __forceinline__ bool find_expert(const W4Params &p, int run_rows, int
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int i = base + 4 * lane + j;
-            raw[j] = i <= p.G ? __ldg(p.offsets + i) : 0;
+            raw[j] = i <= p.G ? p.offsets[i] : 0;
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
