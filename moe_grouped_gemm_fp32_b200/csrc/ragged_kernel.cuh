@@ -101,6 +101,9 @@ struct RaggedParams {
     int M, N, K;              // kTN: output rows M; kNT, kNN: reduced size K
     int G;
     int accumulate;           // kTN: add to d
+    // When the next grid's blocks may be placed: once this grid's blocks are set up, or
+    // each when its tiles are done.  (The first thread of a block that says so counts.)
+    int signal_early;
     int debug_flags;
 };
 
@@ -480,6 +483,7 @@ ragged_gemm_kernel(const __grid_constant__ RaggedMaps<kDir> maps, const RaggedPa
     if constexpr (kPair) ptx::cluster_sync_all();   // the peer's barriers exist before any remote use
     ptx::tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
+    if (p.signal_early && threadIdx.x == 0) pdl::grid_launch_dependents();
 
     const int num_tiles = prefix[p.G];
     const int t_first = static_cast<int>(blockIdx.x) / kCtaGroup;
@@ -787,12 +791,7 @@ ragged_gemm_kernel(const __grid_constant__ RaggedMaps<kDir> maps, const RaggedPa
     // ---------------------------------------------------------------- teardown
     ptx::tc_fence_before();
     __syncthreads();
-    // The next grid's blocks may be placed.  The first thread of a block that says so
-    // counts, so none does before the block's tiles are done: blocks that come while some
-    // SMs are done fill the SMs unevenly (a 4-bit call of 8 tokens, 16384 x 7168, behind a
-    // forward of one expert of 16 rows, 1024 x 1024: 28.3 us for both with the signal at the
-    // end of each warp's own role, which idle warps reach at once, 25.1 here, 25.1 without
-    // it; that forward and its input gradient: 11.4, 11.6, 12.1).
+    // The next grid's blocks may be placed (see RaggedParams::signal_early).
     if (threadIdx.x == 0) pdl::grid_launch_dependents();
     // (After the barrier: a pair's second CTA issues no MMAs, and would wait here from its
     // start, so that the limit bounded the call.)
