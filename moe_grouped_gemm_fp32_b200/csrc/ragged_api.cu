@@ -143,15 +143,15 @@ dg_status_t m_grouped(const void *a, const void *b, void *d, const int32_t *offs
     if (T == 0) return DG_SUCCESS;
     const dg::RaggedParams p = ragged_params(d, offsets, T, 0, N, K, G, 0, info);
     // 256-row CTA pairs where an expert has 128 rows or more on average and there are a
-    // few of their tiles: 8 experts of 128 rows, 2048 x 4096: 32.8 us in pair tiles, 50.3 in
+    // few of their tiles: 8 experts of 128 rows, 2048 x 4096: 34.0 us in pair tiles, 42.6 in
     // single ones; one expert of 512 rows, 1024 x 1024: 8 pair tiles 10.5 us, 64 single
-    // ones 8.5.  Thin tiles of 32 rows where experts have 24 or fewer on average, so that
+    // ones 8.4.  Thin tiles of 32 rows where experts have 24 or fewer on average, so that
     // few need several (16 experts of 4096 x 7168, tiles of 128 rows against thin ones: 24
-    // rows on average, skewed, 154 and 145 us, 48 rows 157 and 169), or where the thin ones
+    // rows on average, skewed, 157 and 146 us, 48 rows 161 and 176), or where the thin ones
     // fill no more than the SMs once: a call of few tiles takes as long as one tile does
-    // (one expert of 256 rows, 1024 x 8192, 128 thin tiles: 32.4 and 18.6; 192 rows, 4096 x
-    // 4096, 384 of them: 19.8 and 26.2).  Tiles 64 wide where 128 would leave SMs without one
-    // (one expert of 16 rows, 4096 x 7168: 16.8 us, 22.7 in the wider ones).
+    // (one expert of 256 rows, 1024 x 8192, 128 thin tiles: 33 and 19.7; 192 rows, 4096 x
+    // 4096, 384 of them: 19.5 and 28.3).  Tiles 64 wide where 128 would leave SMs without one
+    // (one expert of 16 rows, 4096 x 7168: 18.0 us, 23.0 in the wider ones).
     const long long pair_tiles = ceil_div(T, 256) * ceil_div(N, 256);
     const bool pair = N > 128 && T / used >= 128 && 8 * pair_tiles >= info->num_sms;
     const bool thin = !pair && (T / used <= 24 || ceil_div(T, 32) * ceil_div(N, 64) <= info->num_sms);
@@ -174,8 +174,8 @@ dg_status_t m_grouped(const void *a, const void *b, void *d, const int32_t *offs
 // Most tokens of a call whose BF16 weight gradient is summed in one level.  What the
 // tensor core's accumulator then loses, 4.7e-5 of a sum of products of one sign, is 1/80
 // of a BF16 result's half step, and two groups of epilogue warps can take turns: 64
-// experts of 62 tokens, 1000 x 2112, 71.5 us and 77.5 in two levels; 8 experts of 1024
-// tokens, 2048 x 4096, 108.6 and 112.3.
+// experts of 62 tokens, 1000 x 2112, 70.4 us and 77.5 in two levels; of 125, 84.1 and
+// 89.9; 8 experts of 1024 tokens, 2048 x 4096, 107.5 and 109.0.
 constexpr int kOneLevelTokens = 8192;
 
 template <bool kF32, bool kTwoLevel>

@@ -37,8 +37,8 @@
 // boxes (single CTAs of kNT, kNN: 32 weights x 16 tokens) around in shared memory and
 // stores runs of a row.
 //
-// Roles: warp 0 producer (TMA), warp 1 TMEM and MMA issue, warps 4.. epilogue: warp w drains TMEM lanes 32 (w % 4), columns
-// of half (w / 4 - 1) % 2.  Persistent; two accumulators in rotation, so the next
+// Roles: warp 0 producer (TMA), warp 1 TMEM and MMA issue, warps 4.. epilogue: warp w
+// drains TMEM lanes 32 (w % 4), columns of half (w / 4 - 1) % 2.  Persistent; two accumulators in rotation, so the next
 // tile's MMAs overlap this tile's stores; with one-level sums a group of 8 epilogue
 // warps for each, so that tiles of few tokens store two at a time.
 //
@@ -48,12 +48,13 @@
 // that weight bytes, not token tiles, fill the memory pipeline.  Where experts have
 // a few rows, or the call few tiles, they are thin (kRows 32): a stage keeps 4 KB for
 // A and not 16, and twice as many weight bytes are in flight (64 rows over 16 experts,
-// 4096 x 7168: 156 -> 143 us, 98 % of the copy rate).
+// 4096 x 7168, in a graph: 155 us in tiles of 128 rows, 138 in thin ones, the copy rate).
 //
 // Single CTAs of kNT and kNN make the weights the MMA's 128 rows and the tokens its
 // columns, as many as the expert has, rounded up to 16: the other way round, products
-// of rows that no expert has cost time and, in a loop, the clock (those 64 rows: 165 ->
-// 141 us; 64 experts of 62 rows on average, 1000 x 2112: 66 -> 61).  Tiles of 64 weights leave
+// of rows that no expert has cost time and the clock (in a loop of calls, where the GPU
+// is hotter than in a graph of few, those 64 rows: 165 -> 141 us; 64 experts of 62 rows on
+// average, 1000 x 2112: 66 -> 61; both with one-level sums).  Tiles of 64 weights leave
 // the MMA's upper rows whatever follows in shared memory (the next stage, in the middle
 // of being written perhaps); nobody reads those accumulator rows.
 //
@@ -67,7 +68,8 @@
 // seen where one tile's latency is the call's (one expert of 64 rows, 512 x 8192:
 // 17.2 us in one level, 20.4 with 512, 18.8 with 1024, 17.9 with 2048) and not
 // elsewhere (64 rows, 16 experts, 4096 x 7168: 137 each; 64 experts of 62 rows, 1000 x
-// 2112: 59.0 and 59.9).  Only short BF16 weight gradients go without (rule and figures in
+// 2112: 59.0 and 59.9; 32768 rows in a loop 1538 and 1555, whatever the segments'
+// length).  Only short BF16 weight gradients go without (rule and figures in
 // ragged_api.cu).
 //
 // Every wait is bounded (BoundedWait).
@@ -80,7 +82,8 @@ namespace dg {
 
 enum RaggedDir : int { kNT = 0, kNN = 1, kTN = 2 };
 
-// 4 warps that load and multiply, and 8 warps for each accumulator in rotation; two-level sums take one such group, with more registers
+// 4 warps that load and multiply, and 8 warps for each accumulator in rotation;
+// two-level sums take one such group, with more registers
 __host__ __device__ constexpr int ragged_threads(bool two_level) { return two_level ? 384 : 640; }
 constexpr int kRaggedBlockK = 64;
 // Row blocks per L2 raster band at most; an expert's bands are equally high (33 row
@@ -125,7 +128,8 @@ struct RaggedSmem {
     static constexpr int kBBytes = kBCols * 128;
     // K-blocks of 64 in a stage: two in thin tiles of 64 columns, where few tiles wait on
     // a block's barriers and issue (0.2 us) rather than on its bytes: 4 rows, 1024 x
-    // 8192, 26.2 -> 17.6 us; four a stage, of which then three fit: 19.7
+    // 8192, 26.2 -> 17.6 us (18.5 with two-level sums); four a stage, of which then three
+    // fit: 19.7
     static constexpr int kSub = kRows == 32 && kBN == 64 ? 2 : 1;
     static constexpr int kSubBytes = kABytes + kBBytes;
     static constexpr int kStageBytes = kSub * kSubBytes;

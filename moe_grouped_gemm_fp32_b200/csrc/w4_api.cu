@@ -72,7 +72,7 @@ dg_status_t launch_w4(dg::W4Params p, int split, int runs, cudaStream_t stream) 
 // in times that an SM with enough CTAs takes for a block of K.  It works through the blocks
 // of all of its CTAs; a wave of resident ones takes at least the latency of a CTA's blocks,
 // 2.5 such times each (2 with 16 or 32 tokens); and each CTA costs 3 to start and hand over.
-// Measured for 1 to 1000 row blocks, 4 to 128 blocks of K, 1 to 30 tokens (400 shapes, splits
+// Measured for 4 to 1000 row blocks, 4 to 128 blocks of K, 1 to 30 tokens (400 shapes, splits
 // of 1, 2, 4, 8): the choice takes 0.5 % more than the best one on average, 10 % at
 // worst.  512 row blocks of 55 K blocks, one token: 56.1 us whole, 50.1 halved.
 int k_split(long long row_blocks, int k_blocks, int tokens, int num_sms) {
